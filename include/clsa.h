@@ -254,6 +254,147 @@ CLSA_API clsa_status clsa_prefill_attention(const clsa_prefill_args* a, int mode
                                             void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Rotary positions of queries and keys                                       */
+/* ------------------------------------------------------------------------ */
+/* Pair i of the first `rot` elements of every head is turned by a = pos * f_i,
+ *   (x1, x2) -> mscale * (x1 cos a - x2 sin a, x2 cos a + x1 sin a),
+ * elements from `rot` on are copied.  Pairs: CLSA_ROPE_HALF (i, i + rot/2),
+ * CLSA_ROPE_INTERLEAVED (2i, 2i + 1).  f_i = theta^(-2i/rot), changed by `scaling`:
+ *   CLSA_ROPE_PLAIN     as it is
+ *   CLSA_ROPE_LINEAR    f_i / factor
+ *   CLSA_ROPE_BASE      theta * factor^(rot / (rot - 2)) in theta's place
+ *   CLSA_ROPE_BY_PARTS  g f_i + (1 - g) f_i / factor, with r = orig_len f_i / 2 pi turns
+ *                       and g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ * (RoFormer, Su et al. 2021; YaRN, Peng et al. 2023).  inverse != 0 applies the transpose
+ * (-a in a's place, the same mscale): the gradient with respect to the inputs, given the
+ * gradient with respect to the outputs.
+ * q [Nq][Hq][d] and k [Nk][Hk][d] in dtype; row r has position pos[r % n_pos] (pos [n_pos]
+ * device int32, any value).  Nq and Nk are multiples of n_pos: Q [L][B][Hq][d] of L layers
+ * with one position per sequence is Nq = L B, n_pos = B.  q or k may be NULL (its row count
+ * 0); q_out may equal q and k_out may equal k, else no buffer overlaps another.
+ * d in {64, 128}; rot a multiple of 16, 16 <= rot <= d.  Angles are reduced in fp64, sines and
+ * products are fp32, one rounding to dtype.  mscale <= 0 selects 1.  Needs no workspace. */
+typedef enum clsa_rope_layout { CLSA_ROPE_HALF = 0, CLSA_ROPE_INTERLEAVED = 1 } clsa_rope_layout;
+typedef enum clsa_rope_scaling {
+  CLSA_ROPE_PLAIN = 0,
+  CLSA_ROPE_LINEAR = 1,
+  CLSA_ROPE_BASE = 2,
+  CLSA_ROPE_BY_PARTS = 3
+} clsa_rope_scaling;
+typedef struct clsa_rope_args {
+  clsa_dtype dtype;
+  int Nq, Nk, n_pos, Hq, Hk, d, rot;
+  int layout;                /* clsa_rope_layout                                  */
+  int scaling;               /* clsa_rope_scaling                                 */
+  int inverse;
+  int orig_len;              /* by parts: the length trained on, >= 1             */
+  double theta;              /* > 1                                               */
+  double factor;             /* > 0 (not read by CLSA_ROPE_PLAIN)                 */
+  double beta_fast, beta_slow; /* by parts: turns, beta_fast > beta_slow >= 0     */
+  double mscale;             /* <= 0: 1                                           */
+  const void* q;             /* [Nq][Hq][d] or NULL                               */
+  const void* k;             /* [Nk][Hk][d] or NULL                               */
+  const int32_t* pos;        /* [n_pos]                                           */
+  void* q_out;               /* out [Nq][Hq][d], NULL exactly when q is           */
+  void* k_out;               /* out [Nk][Hk][d], NULL exactly when k is           */
+} clsa_rope_args;
+CLSA_API clsa_status clsa_rope(const clsa_rope_args* a, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* 8-bit K/V cache                                                            */
+/* ------------------------------------------------------------------------ */
+/* K8, V8 [B][n_max][Hkv][d] hold e4m3 codes, k_scale, v_scale [B][ceil(n_max / block)][Hkv]
+ * fp32 a scale for each block of tokens and head: a code stands for code * scale.  The scale
+ * is the smallest power of two >= 2^-100 with max |x| / scale <= 448 over the block's finite
+ * elements (at most 2^119).  block in {16, 32, 64, 128}, d in {64, 128}.  The caller owns the
+ * four buffers; they need no initial value: a block's bytes are read only for rows that
+ * were written. */
+typedef struct clsa_kv8_cache {
+  int B, n_max, Hkv, d, block;
+  void* K8;                  /* [B][n_max][Hkv][d] e4m3, 16-byte aligned          */
+  void* V8;
+  float* k_scale;            /* [B][ceil(n_max/block)][Hkv]                       */
+  float* v_scale;
+} clsa_kv8_cache;
+
+/* Quantise new rows K, V [B][T][Hkv][d] (dt) into the cache: row t < count[b] of sequence b
+ * becomes token start[b] + t (count NULL: T rows; counts are clamped to [0, T]).  Codes are
+ * x / scale rounded to nearest even; infinities saturate to +-448, NaN is kept.  Tokens before
+ * start[b] count as written, tokens from start[b] on as free: a block whose first token is
+ * among the new rows gets a new scale; a block that holds earlier rows keeps its scale or
+ * takes a larger one, and then its earlier codes are rounded to that.  Tokens behind the new
+ * rows are left as they were.  A sequence whose rows do not all lie in [0, n_max) is not
+ * written and CLSA_ERR_BAD_INDEX is recorded in ws (detail: b << 32 | start).
+ * ws: clsa_kv8_workspace_size() bytes, for this call and clsa_kv8_read. */
+CLSA_API size_t clsa_kv8_workspace_size(void);
+CLSA_API clsa_status clsa_kv8_write(const clsa_kv8_cache* cache, const void* K, const void* V, const int32_t* start,
+                                    const int32_t* count, int T, clsa_dtype dt, void* ws, size_t ws_bytes,
+                                    void* stream);
+/* Read rows back into K, V [B][T][Hkv][d] (dt): row t < count[b] (NULL: T) is token
+ * idx[b][t] (idx [B][T], e.g. clsa_topk's, giving clsa_sparse_attn's compact rows), or where
+ * idx is NULL token start[b] + t (start NULL: 0; not both).  Rows from count[b] on are left as they
+ * were.  A token outside [0, n_max) is not read: its row is zero-filled and
+ * CLSA_ERR_BAD_INDEX is recorded in ws (detail: b << 32 | t). */
+CLSA_API clsa_status clsa_kv8_read(const clsa_kv8_cache* cache, const int32_t* start, const int32_t* idx,
+                                   const int32_t* count, int T, clsa_dtype dt, void* K, void* V, void* ws,
+                                   size_t ws_bytes, void* stream);
+
+/* Attention over the 8-bit cache: O^(l)[b] = softmax(Q^(l)[b] K^T * scale) V with K and V
+ * the cache's code * scale values.  Q [L][B][Hq][d] in dtype (bf16 or fp32); Hq a multiple of
+ * cache.Hkv; lse [L][B][Hq] fp32 out (natural log), may be NULL.
+ * idx NULL: sequence b attends over its tokens [0, count[b]) (counts clamped to [0, n_max]).
+ * idx [B][k]: over the tokens idx[b][0 .. count[b]) (counts clamped to [0, k]; 1 <= k <= 2^24), e.g.
+ * clsa_topk's selection, read straight from the cache.  A token outside [0, n_max) is left out
+ * and CLSA_ERR_BAD_INDEX is recorded in ws (detail: b << 32 | position).
+ * cache.B is B, or 1: then the one cache serves every b (rows of a prefill chunk, each with
+ * its own count or selection).  A row that sees no token gets O = 0 and lse = -inf.
+ * Scales are taken to be powers of two, as clsa_kv8_write makes them.  Scores, sums and outputs
+ * accumulate in fp32; probabilities enter the second product as halves relative to the row's
+ * largest (two halves, 22 bits, for fp32).  Deterministic.  One launch.
+ * ws: clsa_kv8_attn_workspace_size(a) bytes (0: arguments the call would reject). */
+typedef struct clsa_kv8_attn_args {
+  clsa_dtype dtype;
+  int B, L, Hq, k;           /* k: row length of idx (not read where idx is NULL)  */
+  float scale;               /* <= 0: 1/sqrt(d)                                   */
+  clsa_kv8_cache cache;
+  const void* Q;             /* [L][B][Hq][d]                                     */
+  const int32_t* idx;        /* [B][k] or NULL                                    */
+  const int32_t* count;      /* [B]                                               */
+  void* O;                   /* out [L][B][Hq][d]                                 */
+  float* lse;                /* out [L][B][Hq] or NULL                            */
+} clsa_kv8_attn_args;
+CLSA_API size_t clsa_kv8_attn_workspace_size(const clsa_kv8_attn_args* a);
+CLSA_API clsa_status clsa_kv8_attn(const clsa_kv8_attn_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention with a sliding window and sink tokens                            */
+/* ------------------------------------------------------------------------ */
+/* The T newest tokens of each sequence attend over its cache K, V [B][n_max][Hkv][d], which
+ * holds seq_lens[b] tokens, theirs among them (lengths are clamped to [0, n_max]).  Row t of
+ * Q [B][T][Hq][d] stands at position p = seq_lens[b] - T + t and sees the tokens
+ *   j <= p  with  j > p - window  or  j < sinks        (window >= 1, sinks >= 0).
+ * T = 1 is the decode step.  Where seq_lens[b] < T the first T - seq_lens[b] rows are padding:
+ * they see nothing and get O = 0, lse = -inf.  Tokens that no row of a call sees are not
+ * part of it, whatever their bytes.  Among those that some row sees, a NaN or infinity in V
+ * can reach other rows of the call too (0 * NaN); K's stay with the rows that see them.
+ * O [B][T][Hq][d] and lse [B][T][Hq] (fp32, natural log, may be NULL) out; query head h reads
+ * KV head h / (Hq / Hkv).  dtype bf16 or fp32 (fp32 products).  Deterministic.  One launch.
+ * ws: clsa_window_attn_workspace_size(a) bytes (0: arguments the call would reject). */
+typedef struct clsa_window_args {
+  clsa_dtype dtype;
+  int B, T, n_max, Hq, Hkv, d, window, sinks;
+  float scale;               /* <= 0: 1/sqrt(d)                                   */
+  const void* Q;             /* [B][T][Hq][d]                                     */
+  const void* K;             /* [B][n_max][Hkv][d]                                */
+  const void* V;
+  const int32_t* seq_lens;   /* [B]                                               */
+  void* O;                   /* out [B][T][Hq][d]                                 */
+  float* lse;                /* out [B][T][Hq] or NULL                            */
+} clsa_window_args;
+CLSA_API size_t clsa_window_attn_workspace_size(const clsa_window_args* a);
+CLSA_API clsa_status clsa_window_attn(const clsa_window_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------ */
 /* Helpers                                                                    */
 /* ------------------------------------------------------------------------ */
 /* Workspace bytes of an operation, given its argument struct: op CLSA_OP_DECODE_STEP

@@ -32,6 +32,8 @@ EXPORTS = [
     "clsa_prefill_chunk", "clsa_prefill_attention", "clsa_workspace_size", "clsa_workspace_init", "clsa_read_device_status", "clsa_status_string",
     "clsa_selftest_timeout", "clsa_version", "clsa_last_launch_count", "clsa_time_next_call",
     "clsa_timed_event_count",
+    "clsa_rope", "clsa_kv8_workspace_size", "clsa_kv8_write", "clsa_kv8_read",
+    "clsa_kv8_attn_workspace_size", "clsa_kv8_attn", "clsa_window_attn_workspace_size", "clsa_window_attn",
 ]
 
 
@@ -43,6 +45,7 @@ class ClsaError(RuntimeError):
 
 
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_d = ctypes.c_double
 
 
 class DecodeArgs(ctypes.Structure):
@@ -58,6 +61,29 @@ class PrefillArgs(ctypes.Structure):
                 ("Hq", _i), ("Hkv", _i), ("d", _i), ("scale", _f),
                 ("q_idx", _vp), ("k_idx", _vp), ("K", _vp), ("V", _vp), ("Q", _vp),
                 ("O", _vp), ("idx", _vp), ("count", _vp), ("lse", _vp)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("Nq", _i), ("Nk", _i), ("n_pos", _i), ("Hq", _i), ("Hk", _i), ("d", _i),
+                ("rot", _i), ("layout", _i), ("scaling", _i), ("inverse", _i), ("orig_len", _i),
+                ("theta", _d), ("factor", _d), ("beta_fast", _d), ("beta_slow", _d), ("mscale", _d),
+                ("q", _vp), ("k", _vp), ("pos", _vp), ("q_out", _vp), ("k_out", _vp)]
+
+
+class Kv8CacheArgs(ctypes.Structure):
+    _fields_ = [("B", _i), ("n_max", _i), ("Hkv", _i), ("d", _i), ("block", _i),
+                ("K8", _vp), ("V8", _vp), ("k_scale", _vp), ("v_scale", _vp)]
+
+
+class Kv8AttnArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("B", _i), ("L", _i), ("Hq", _i), ("k", _i), ("scale", _f), ("cache", Kv8CacheArgs),
+                ("Q", _vp), ("idx", _vp), ("count", _vp), ("O", _vp), ("lse", _vp)]
+
+
+class WindowArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i), ("B", _i), ("T", _i), ("n_max", _i), ("Hq", _i), ("Hkv", _i), ("d", _i),
+                ("window", _i), ("sinks", _i), ("scale", _f),
+                ("Q", _vp), ("K", _vp), ("V", _vp), ("seq_lens", _vp), ("O", _vp), ("lse", _vp)]
 
 
 _lib = None
@@ -101,6 +127,14 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "clsa_last_launch_count": (_i, []),
         "clsa_time_next_call": (S, [ctypes.POINTER(ctypes.c_void_p), _i]),
         "clsa_timed_event_count": (_i, []),
+        "clsa_rope": (S, [ctypes.POINTER(RopeArgs), _vp]),
+        "clsa_kv8_workspace_size": (_sz, []),
+        "clsa_kv8_write": (S, [ctypes.POINTER(Kv8CacheArgs), _vp, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+        "clsa_kv8_read": (S, [ctypes.POINTER(Kv8CacheArgs), _vp, _vp, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+        "clsa_kv8_attn_workspace_size": (_sz, [ctypes.POINTER(Kv8AttnArgs)]),
+        "clsa_kv8_attn": (S, [ctypes.POINTER(Kv8AttnArgs), _vp, _sz, _vp]),
+        "clsa_window_attn_workspace_size": (_sz, [ctypes.POINTER(WindowArgs)]),
+        "clsa_window_attn": (S, [ctypes.POINTER(WindowArgs), _vp, _sz, _vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -402,6 +436,195 @@ def prefill_attention(q_idx, k_idx, K, V, Q, k, idx, count, mode: int = 0, scale
     ws = (ws or Workspace(need)).ensure(need)
     _check(load_library().clsa_prefill_attention(ctypes.byref(a), int(mode), ws.ptr, ws.nbytes, _stream()),
            "clsa_prefill_attention")
+    return O, lse
+
+
+# ---------------------------------------------------------------------------- positions, 8-bit cache
+
+def _here(t: Optional[torch.Tensor], what: str, shape=None, dtype=None):
+    """The address of a contiguous tensor on the current device, of the given shape and dtype."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {dtype} is wanted, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+_ROPE_LAYOUT = {"half": 0, "interleaved": 1}
+_ROPE_SCALING = {"plain": 0, "linear": 1, "base": 2, "by_parts": 3}
+
+
+def rope(q, k, pos, rot: Optional[int] = None, layout: str = "half", theta: float = 10000.0, scaling: str = "plain",
+         factor: float = 1.0, orig_len: int = 1, beta_fast: float = 32.0, beta_slow: float = 1.0, mscale: float = 1.0,
+         inverse: bool = False, q_out=None, k_out=None):
+    """Rotary positions (see clsa.h): q [..., Hq, d] and k [..., Hk, d] (either may be None), pos
+    int32 [n_pos]; the rows before the heads run over positions with pos fastest, so Q [L][B][Hq][d]
+    takes pos [B].  inverse=True is the transpose (the gradient).  Returns (q_out, k_out);
+    q_out=q and k_out=k work in place."""
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q and k are both None")
+    d, dt = x.shape[-1], x.dtype
+    n_pos = pos.numel()
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+    Hq, Hk = (q.shape[-2] if q is not None else 0), (k.shape[-2] if k is not None else 0)
+    if k is not None and k.shape[-1] != d:
+        raise ValueError(f"k: head dimension {d} is wanted, got {k.shape[-1]}")
+    a = RopeArgs(_dt(x), q.numel() // (Hq * d) if Hq else 0, k.numel() // (Hk * d) if Hk else 0, n_pos, Hq, Hk, d,
+                 d if rot is None else rot, _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], bool(inverse), orig_len,
+                 theta, factor, beta_fast, beta_slow, mscale, _here(q, "q", None, dt), _here(k, "k", None, dt),
+                 _here(pos, "pos", None, torch.int32), _here(q_out, "q_out", q.shape if q is not None else None, dt),
+                 _here(k_out, "k_out", k.shape if k is not None else None, dt))
+    _check(load_library().clsa_rope(ctypes.byref(a), _stream()), "clsa_rope")
+    return q_out, k_out
+
+
+class Kv8Cache:
+    """Handle of an 8-bit K/V cache (see clsa.h): codes K8, V8 [B][n_max][Hkv][d] (torch.float8_e4m3fn
+    or uint8) and scales k_scale, v_scale fp32 [B][ceil(n_max / block)][Hkv].  It holds the tensors."""
+
+    def __init__(self, K8, V8, k_scale, v_scale, block: int = 64):
+        if K8.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise TypeError(f"K8: torch.float8_e4m3fn or torch.uint8 is wanted, got {K8.dtype}")
+        self.B, self.n_max, self.Hkv, self.d = K8.shape
+        self.block = int(block)
+        self.K8, self.V8, self.k_scale, self.v_scale = K8, V8, k_scale, v_scale
+        scales = (self.B, -(-self.n_max // max(self.block, 1)), self.Hkv)
+        self.args = Kv8CacheArgs(self.B, self.n_max, self.Hkv, self.d, self.block, _here(K8, "K8"),
+                                 _here(V8, "V8", K8.shape, K8.dtype), _here(k_scale, "k_scale", scales, torch.float32),
+                                 _here(v_scale, "v_scale", scales, torch.float32))
+        self._ref = ctypes.byref(self.args)
+
+    @classmethod
+    def empty(cls, B: int, n_max: int, Hkv: int, d: int, block: int = 64, device=None) -> "Kv8Cache":
+        """A cache that holds nothing yet (its bytes are zero)."""
+        dev = device or "cuda"
+        codes = [torch.zeros(B, n_max, Hkv, d, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+        scales = [torch.zeros(B, -(-n_max // block), Hkv, dtype=torch.float32, device=dev) for _ in range(2)]
+        return cls(*codes, *scales, block)
+
+
+def kv8_write(cache: Kv8Cache, K, V, start, count=None, ws: Optional[Workspace] = None) -> Kv8Cache:
+    """Quantise K, V [B][T][Hkv][d] into the cache as tokens start[b] + t, t < count[b] (see clsa.h)."""
+    lib = load_library()
+    T = K.shape[1]
+    shape = (cache.B, T, cache.Hkv, cache.d)
+    ws = ws or Workspace(lib.clsa_kv8_workspace_size(), K.device)
+    _check(lib.clsa_kv8_write(cache._ref, _here(K, "K", shape), _here(V, "V", shape, K.dtype),
+                              _here(start, "start", (cache.B,), torch.int32),
+                              _here(count, "count", (cache.B,), torch.int32), T, _dt(K), ws.ptr, ws.nbytes, _stream()),
+           "clsa_kv8_write")
+    return cache
+
+
+def kv8_read(cache: Kv8Cache, K=None, V=None, start=None, idx=None, count=None, T: Optional[int] = None,
+             dtype=torch.bfloat16, ws: Optional[Workspace] = None):
+    """Rows of the cache as K, V [B][T][Hkv][d]: tokens idx[b][t], or start[b] + t (see clsa.h).
+    K and V may be given (rows from count[b] on are left alone); else they start as zeros."""
+    lib = load_library()
+    if K is None:
+        T = idx.shape[1] if idx is not None else T
+        if T is None:
+            raise ValueError("T, idx or K is wanted")
+        K = torch.zeros(cache.B, T, cache.Hkv, cache.d, dtype=dtype, device=cache.K8.device)
+    if V is None:
+        V = torch.zeros_like(K)
+    T = K.shape[1]
+    shape = (cache.B, T, cache.Hkv, cache.d)
+    ws = ws or Workspace(lib.clsa_kv8_workspace_size(), K.device)
+    _check(lib.clsa_kv8_read(cache._ref, _here(start, "start", (cache.B,), torch.int32),
+                             _here(idx, "idx", (cache.B, T), torch.int32),
+                             _here(count, "count", (cache.B,), torch.int32), T, _dt(K), _here(K, "K", shape),
+                             _here(V, "V", shape, K.dtype), ws.ptr, ws.nbytes, _stream()), "clsa_kv8_read")
+    return K, V
+
+
+def _kv8_attn_args(Q, cache, count, idx, scale, O, lse) -> Kv8AttnArgs:
+    L, B, Hq, d = Q.shape
+    if d != cache.d:
+        raise ValueError(f"Q: head dimension {cache.d} is wanted, got {d}")
+    if idx is not None and (idx.dim() != 2 or idx.shape[0] != B):
+        raise ValueError(f"idx: shape [{B}][k] is wanted, got {tuple(idx.shape)}")
+    return Kv8AttnArgs(_dt(Q), B, L, Hq, idx.shape[1] if idx is not None else 0, scale, cache.args, _here(Q, "Q"),
+                       _here(idx, "idx", None, torch.int32), _here(count, "count", (B,), torch.int32),
+                       _here(O, "O", Q.shape, Q.dtype), _here(lse, "lse", (L, B, Hq), torch.float32))
+
+
+def _need(size: int, where: str) -> int:
+    if size == 0:  # the arguments are refused: the size calls do not say why
+        raise ClsaError(1, where)
+    return size
+
+
+def kv8_attn_workspace_size(Q, cache: Kv8Cache, idx=None) -> int:
+    """Workspace bytes of kv8_attn for these tensors (Q [L][B][Hq][d] or [B][Hq][d])."""
+    Qv = Q.unsqueeze(0) if Q.dim() == 3 else Q
+    a = _kv8_attn_args(Qv, cache, None, idx, 0.0, Qv, None)
+    a.count = a.Q  # any aligned address: the size does not read it
+    return _need(load_library().clsa_kv8_attn_workspace_size(ctypes.byref(a)), "clsa_kv8_attn_workspace_size")
+
+
+def kv8_attn(Q, cache: Kv8Cache, count, idx=None, scale: float = 0.0, ws: Optional[Workspace] = None, O=None, lse=None,
+             want_lse: bool = True):
+    """Attention over the 8-bit cache (see clsa.h).  Q [L][B][Hq][d] (or [B][Hq][d] for one layer);
+    count int32 [B] cached tokens, or with idx int32 [B][k] selected ones.  cache.B is B or 1.
+    Returns (O, lse), shaped as Q (lse without d; None where not wanted)."""
+    lib = load_library()
+    squeeze = Q.dim() == 3
+    if squeeze:
+        Q, O, lse = Q.unsqueeze(0), O if O is None else O.unsqueeze(0), lse if lse is None else lse.unsqueeze(0)
+    if O is None:
+        O = torch.empty_like(Q)
+    if lse is None and want_lse:
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    a = _kv8_attn_args(Q, cache, count, idx, scale, O, lse)
+    ref = ctypes.byref(a)
+    if ws is None:
+        ws = Workspace(_need(lib.clsa_kv8_attn_workspace_size(ref), "clsa_kv8_attn_workspace_size"), Q.device)
+    _check(lib.clsa_kv8_attn(ref, ws.ptr, ws.nbytes, _stream()), "clsa_kv8_attn")
+    return (O[0], lse[0] if lse is not None else None) if squeeze else (O, lse)
+
+
+def _window_args(Q, K, V, seq_lens, window, sinks, scale, O, lse) -> WindowArgs:
+    B, T, Hq, d = Q.shape
+    n_max, Hkv = K.shape[1], K.shape[2]
+    shape = (B, n_max, Hkv, d)
+    return WindowArgs(_dt(Q), B, T, n_max, Hq, Hkv, d, window, sinks, scale, _here(Q, "Q"),
+                      _here(K, "K", shape, Q.dtype), _here(V, "V", shape, Q.dtype),
+                      _here(seq_lens, "seq_lens", (B,), torch.int32), _here(O, "O", Q.shape, Q.dtype),
+                      _here(lse, "lse", (B, T, Hq), torch.float32))
+
+
+def window_attn_workspace_size(Q, K, window: int, sinks: int = 0) -> int:
+    """Workspace bytes of window_attn for these tensors."""
+    a = _window_args(Q, K, K, None, window, sinks, 0.0, Q, None)
+    a.seq_lens = a.Q  # any aligned address: the size does not read it
+    return _need(load_library().clsa_window_attn_workspace_size(ctypes.byref(a)), "clsa_window_attn_workspace_size")
+
+
+def window_attn(Q, K, V, seq_lens, window: int, sinks: int = 0, scale: float = 0.0, ws: Optional[Workspace] = None,
+                O=None, lse=None, want_lse: bool = True):
+    """Attention of the T newest tokens of each sequence with a sliding window and sink tokens (see
+    clsa.h): Q [B][T][Hq][d], K, V [B][n_max][Hkv][d], seq_lens int32 [B].  Returns (O, lse)."""
+    lib = load_library()
+    if O is None:
+        O = torch.empty_like(Q)
+    if lse is None and want_lse:
+        lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
+    a = _window_args(Q, K, V, seq_lens, window, sinks, scale, O, lse)
+    ref = ctypes.byref(a)
+    if ws is None:
+        ws = Workspace(_need(lib.clsa_window_attn_workspace_size(ref), "clsa_window_attn_workspace_size"), Q.device)
+    _check(lib.clsa_window_attn(ref, ws.ptr, ws.nbytes, _stream()), "clsa_window_attn")
     return O, lse
 
 

@@ -104,6 +104,51 @@ clsa_status check_decode(const clsa_decode_args* a) {
   return CLSA_OK;
 }
 
+clsa_status check_kv8(const clsa_kv8_cache* c) {
+  if (!c || c->B < 1 || c->n_max < 1 || c->Hkv < 1) return CLSA_ERR_INVALID_ARG;
+  if (!c->K8 || !c->V8 || !c->k_scale || !c->v_scale) return CLSA_ERR_INVALID_ARG;
+  if (!dims_ok(c->d)) return CLSA_ERR_UNSUPPORTED;
+  if (c->block != 16 && c->block != 32 && c->block != 64 && c->block != 128) return CLSA_ERR_UNSUPPORTED;
+  if (c->n_max > (1 << 30) || c->Hkv > (1 << 16)) return CLSA_ERR_UNSUPPORTED;
+  if (!aligned16(c->K8) || !aligned16(c->V8) || !aligned4(c->k_scale) || !aligned4(c->v_scale))
+    return CLSA_ERR_INVALID_ARG;
+  return CLSA_OK;
+}
+
+// sizes that the streaming attention counts in 32 bits: rows of a KV head, (sequence, row) pairs
+constexpr long long kMaxStreamRows = 1LL << 24;
+
+clsa_status check_kv8_attn(const clsa_kv8_attn_args* a) {
+  if (!a) return CLSA_ERR_INVALID_ARG;
+  const clsa_status st = check_kv8(&a->cache);
+  if (st != CLSA_OK) return st;
+  if (a->B < 1 || a->L < 1 || a->Hq < 1 || !dtype_ok(a->dtype)) return CLSA_ERR_INVALID_ARG;
+  if (a->cache.B != a->B && a->cache.B != 1) return CLSA_ERR_INVALID_ARG;
+  if (!a->Q || !a->count || !a->O || (a->idx && a->k < 1)) return CLSA_ERR_INVALID_ARG;
+  if (a->Hq % a->cache.Hkv != 0 || (a->idx && a->k > kMaxDirectK)) return CLSA_ERR_UNSUPPORTED;
+  if ((long long)a->L * a->Hq > kMaxStreamRows || (long long)a->B * a->L * a->Hq > 8 * kMaxStreamRows)
+    return CLSA_ERR_UNSUPPORTED;
+  if (!aligned16(a->Q) || !aligned16(a->O)) return CLSA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->idx, (const void*)a->count, (const void*)a->lse})
+    if (p && !aligned4(p)) return CLSA_ERR_INVALID_ARG;
+  return CLSA_OK;
+}
+
+clsa_status check_window(const clsa_window_args* a) {
+  if (!a || a->B < 1 || a->T < 1 || a->n_max < 1 || a->Hq < 1 || a->Hkv < 1 || a->window < 1 || a->sinks < 0)
+    return CLSA_ERR_INVALID_ARG;
+  if (!dtype_ok(a->dtype)) return CLSA_ERR_INVALID_ARG;
+  if (!a->Q || !a->K || !a->V || !a->seq_lens || !a->O) return CLSA_ERR_INVALID_ARG;
+  if (!dims_ok(a->d) || a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > 128) return CLSA_ERR_UNSUPPORTED;
+  if (a->n_max > (1 << 30) || a->T > (1 << 30)) return CLSA_ERR_UNSUPPORTED;
+  if ((long long)a->T * a->Hq > 8 * kMaxStreamRows || (long long)a->B * a->T * a->Hq > 64 * kMaxStreamRows)
+    return CLSA_ERR_UNSUPPORTED;
+  for (const void* p : {a->Q, a->K, a->V, (const void*)a->O})
+    if (!aligned16(p)) return CLSA_ERR_INVALID_ARG;
+  if (!aligned4(a->seq_lens) || (a->lse && !aligned4(a->lse))) return CLSA_ERR_INVALID_ARG;
+  return CLSA_OK;
+}
+
 float resolve_scale(float scale, int d) { return scale > 0.f ? scale : 1.0f / std::sqrt((float)d); }
 
 }  // namespace
@@ -287,6 +332,91 @@ clsa_status clsa_sparse_attn(const void* Q, const void* K_S, const void* V_S, co
   char* w = static_cast<char*>(ws);
   return from_cuda(launch_sparse_attn(sh, Q, K_S, V_S, nullptr, count, resolve_scale(scale, d), O, lse, w,
                                       w + kWsHeader, static_cast<cudaStream_t>(stream)));
+}
+
+clsa_status clsa_rope(const clsa_rope_args* a, void* stream) {
+  CallScope scope(stream);
+  if (!a || !dtype_ok(a->dtype) || a->n_pos < 1 || a->Nq < 0 || a->Nk < 0 || !a->pos) return CLSA_ERR_INVALID_ARG;
+  if ((a->q != nullptr) != (a->q_out != nullptr) || (a->k != nullptr) != (a->k_out != nullptr) || (!a->q && !a->k))
+    return CLSA_ERR_INVALID_ARG;
+  if ((a->q != nullptr) != (a->Nq > 0) || (a->k != nullptr) != (a->Nk > 0)) return CLSA_ERR_INVALID_ARG;
+  if (a->Nq % a->n_pos != 0 || a->Nk % a->n_pos != 0) return CLSA_ERR_INVALID_ARG;
+  if ((a->q && a->Hq < 1) || (a->k && a->Hk < 1)) return CLSA_ERR_INVALID_ARG;
+  if (a->layout != CLSA_ROPE_HALF && a->layout != CLSA_ROPE_INTERLEAVED) return CLSA_ERR_INVALID_ARG;
+  if (a->scaling < CLSA_ROPE_PLAIN || a->scaling > CLSA_ROPE_BY_PARTS) return CLSA_ERR_INVALID_ARG;
+  if (!(a->theta > 1.0) || !std::isfinite(a->theta) || !std::isfinite(a->mscale)) return CLSA_ERR_INVALID_ARG;
+  if (a->scaling != CLSA_ROPE_PLAIN && (!(a->factor > 0.0) || !std::isfinite(a->factor))) return CLSA_ERR_INVALID_ARG;
+  if (a->scaling == CLSA_ROPE_BY_PARTS &&
+      (a->orig_len < 1 || !(a->beta_slow >= 0.0) || !(a->beta_fast > a->beta_slow) || !std::isfinite(a->beta_fast)))
+    return CLSA_ERR_INVALID_ARG;
+  if (!dims_ok(a->d) || a->rot < 16 || a->rot > a->d || a->rot % 16 != 0) return CLSA_ERR_UNSUPPORTED;
+  // the heads of one position: units are counted in 32 bits
+  if (a->n_pos > (1 << 30) ||
+      (a->q ? (long long)(a->Nq / a->n_pos) * a->Hq : 0) + (a->k ? (long long)(a->Nk / a->n_pos) * a->Hk : 0) >
+          (1 << 24))
+    return CLSA_ERR_UNSUPPORTED;
+  for (const void* p : {a->q, a->k, (const void*)a->q_out, (const void*)a->k_out})
+    if (p && !aligned16(p)) return CLSA_ERR_INVALID_ARG;
+  if (!aligned4(a->pos)) return CLSA_ERR_INVALID_ARG;
+  return from_cuda(launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+size_t clsa_kv8_workspace_size(void) { return kWsHeader; }
+
+clsa_status clsa_kv8_write(const clsa_kv8_cache* c, const void* K, const void* V, const int32_t* start,
+                           const int32_t* count, int T, clsa_dtype dt, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope(stream);
+  const clsa_status st = check_kv8(c);
+  if (st != CLSA_OK) return st;
+  if (!K || !V || !start || T < 1 || !dtype_ok(dt)) return CLSA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V) || !aligned4(start) || (count && !aligned4(count))) return CLSA_ERR_INVALID_ARG;
+  if (!kv8_write_grid_ok(c, T)) return CLSA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < kWsHeader || !aligned16(ws)) return CLSA_ERR_WORKSPACE;
+  return from_cuda(launch_kv8_write(c, K, V, start, count, T, dt, ws, static_cast<cudaStream_t>(stream)));
+}
+
+clsa_status clsa_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const int32_t* idx, const int32_t* count,
+                          int T, clsa_dtype dt, void* K, void* V, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope(stream);
+  const clsa_status st = check_kv8(c);
+  if (st != CLSA_OK) return st;
+  if (!K || !V || T < 1 || !dtype_ok(dt) || (start && idx)) return CLSA_ERR_INVALID_ARG;
+  if (!aligned16(K) || !aligned16(V)) return CLSA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)start, (const void*)idx, (const void*)count})
+    if (p && !aligned4(p)) return CLSA_ERR_INVALID_ARG;
+  if (!kv8_read_grid_ok(c, T)) return CLSA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < kWsHeader || !aligned16(ws)) return CLSA_ERR_WORKSPACE;
+  return from_cuda(launch_kv8_read(c, start, idx, count, T, dt, K, V, ws, static_cast<cudaStream_t>(stream)));
+}
+
+size_t clsa_kv8_attn_workspace_size(const clsa_kv8_attn_args* a) {
+  if (check_kv8_attn(a) != CLSA_OK) return 0;
+  return kWsHeader + kv8_attn_ws_bytes(a);
+}
+
+clsa_status clsa_kv8_attn(const clsa_kv8_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope(stream);
+  const clsa_status st = check_kv8_attn(a);
+  if (st != CLSA_OK) return st;
+  if (!ws || ws_bytes < kWsHeader + kv8_attn_ws_bytes(a) || !aligned16(ws)) return CLSA_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  return from_cuda(launch_kv8_attn(a, resolve_scale(a->scale, a->cache.d), w, w + kWsHeader,
+                                   static_cast<cudaStream_t>(stream)));
+}
+
+size_t clsa_window_attn_workspace_size(const clsa_window_args* a) {
+  if (check_window(a) != CLSA_OK) return 0;
+  return kWsHeader + window_attn_ws_bytes(a);
+}
+
+clsa_status clsa_window_attn(const clsa_window_args* a, void* ws, size_t ws_bytes, void* stream) {
+  CallScope scope(stream);
+  const clsa_status st = check_window(a);
+  if (st != CLSA_OK) return st;
+  if (!ws || ws_bytes < kWsHeader + window_attn_ws_bytes(a) || !aligned16(ws)) return CLSA_ERR_WORKSPACE;
+  char* w = static_cast<char*>(ws);
+  return from_cuda(launch_window_attn(a, resolve_scale(a->scale, a->d), w, w + kWsHeader,
+                                      static_cast<cudaStream_t>(stream)));
 }
 
 size_t clsa_distill_workspace_size(int B, int n_max, int L, int Hq, int Hkv, int d) {

@@ -107,6 +107,24 @@ cudaError_t launch_attention_mass_tc(const void* Q, const void* K, const float* 
                                      int n_max, int L, int Hq, int Hkv, float scale, float* mass, float* lse_all,
                                      void* ws_header, void* ws, cudaStream_t s);
 
+// ----- rotary positions ------------------------------------------------------
+cudaError_t launch_rope(const clsa_rope_args* a, cudaStream_t s);
+
+// ----- 8-bit K/V cache: write, read back ----------------------------------------
+// *_grid_ok: the launch fits a 1-D grid
+bool kv8_write_grid_ok(const clsa_kv8_cache* c, int T);
+cudaError_t launch_kv8_write(const clsa_kv8_cache* c, const void* K, const void* V, const int32_t* start,
+                             const int32_t* count, int T, clsa_dtype dt, void* ws_header, cudaStream_t s);
+bool kv8_read_grid_ok(const clsa_kv8_cache* c, int T);
+cudaError_t launch_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const int32_t* idx, const int32_t* count,
+                            int T, clsa_dtype dt, void* K, void* V, void* ws_header, cudaStream_t s);
+
+// ----- attention over the 8-bit cache; attention with a window and sinks --------
+size_t kv8_attn_ws_bytes(const clsa_kv8_attn_args* a);
+cudaError_t launch_kv8_attn(const clsa_kv8_attn_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s);
+size_t window_attn_ws_bytes(const clsa_window_args* a);
+cudaError_t launch_window_attn(const clsa_window_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s);
+
 // ----- failure-detection self-test (a wait that runs out and reports) ------------
 cudaError_t launch_selftest_timeout(int which, void* ws_header, void* ws_body, cudaStream_t s);
 

@@ -1,0 +1,334 @@
+// The 8-bit K/V cache: quantising rows as they are written, and reading rows back.
+//
+// A cache [n][Hkv][d] holds e4m3 codes; each block of `block` tokens and head has a scale
+//   s = the smallest power of two >= 2^-100 with max |x| / s <= 448    (at most 2^119)
+// and a code stands for code * s.  e4m3 is a floating format, so its relative step (2^-3 of
+// the binade) does not depend on s: a power of two loses nothing against max|x| / 448.  It
+// gains that x / s is exact, and that codes already in a block are only shifted when a
+// larger row joins it: code * (s_old / s_new) is exact but where it becomes subnormal, so a
+// cache filled token by token holds what one filled at once holds, up to those.
+//
+// Both kernels move bytes: HBM (long runs) or launch latency (a decode step) is the bound.
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace clsa {
+
+namespace {
+
+constexpr int kThreadsW = 256;
+
+// 16 elements of a row, as floats
+template <typename T> struct Load16;
+template <> struct Load16<__nv_bfloat16> {
+  uint4 v[2];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    v[0] = ld_stream_v4(p);
+    v[1] = ld_stream_v4(p + 8);
+  }
+  __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ float2 pair(int i) const {  // elements 2 i, 2 i + 1
+    const uint4& q = v[i >> 2];
+    const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+    float2 r;
+    unpack_bf16x2(w, r.x, r.y);
+    return r;
+  }
+};
+template <> struct Load16<float> {
+  uint4 v[4];
+  __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = ld_stream_v4(p + 4 * i);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ float2 pair(int i) const {
+    const uint4& q = v[i >> 1];
+    return (i & 1) ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
+                   : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+  }
+};
+
+__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
+  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
+  return u < 0x7f800000u ? u : 0u;
+}
+
+struct WriteParams {
+  const void* K;           // [B][T][Hkv][d] new rows
+  const void* V;
+  const int32_t* start;    // [B]
+  const int32_t* count;    // [B] or null: T rows
+  uint8_t* K8;             // [B][n_max][Hkv][d]
+  uint8_t* V8;
+  float* ks;               // [B][nblk][Hkv]
+  float* vs;
+  void* ws_header;
+  int B, T, n_max, Hkv, d, block, nblk, jmax;
+};
+
+// One CTA per (sequence, block of tokens that the new rows touch, head, K or V): the block's
+// new rows stay in registers between their maximum and their codes, so they are read once.
+// A thread holds NU units of 16 elements.  No two CTAs share a block's scale or codes.
+template <typename T, int NU>
+__global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams p) {
+  pdl_enter();
+  __shared__ uint32_t s_max[kThreadsW / 32];
+  unsigned u = blockIdx.x;  // (which, head, j, b), which fastest
+  const bool isv = u & 1u;
+  u >>= 1;
+  const int h = u % p.Hkv;
+  u /= p.Hkv;
+  const int j = u % p.jmax;
+  const int b = u / p.jmax;
+  const int p0 = p.start[b];
+  const int cnt = p.count ? max(0, min(p.count[b], p.T)) : p.T;
+  if (cnt == 0) return;
+  if (p0 < 0 || p0 > p.n_max - cnt) {  // not all rows fit: none is written
+    if (j == 0 && h == 0 && !isv && threadIdx.x == 0)
+      record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)p0);
+    return;
+  }
+  const int blk = p0 / p.block + j;
+  if (j > (p0 + cnt - 1) / p.block - p0 / p.block) return;  // behind the last block touched
+  const int first = blk * p.block;         // the block's first token
+  const int lo = max(first, p0);           // new rows of this block: tokens [lo, hi)
+  const int hi = min(first + p.block, p0 + cnt);
+  const int upr = p.d / 16;                // units per row
+  const int units = (hi - lo) * upr;
+  const T* src = static_cast<const T*>(isv ? p.V : p.K) + (((size_t)b * p.T + (lo - p0)) * p.Hkv + h) * p.d;
+  const size_t rstr = (size_t)p.Hkv * p.d;
+  uint8_t* codes = (isv ? p.V8 : p.K8) + ((size_t)b * p.n_max * p.Hkv + h) * p.d;
+  float* sc = (isv ? p.vs : p.ks) + ((size_t)b * p.nblk + blk) * p.Hkv + h;
+  const bool kept = lo > first;            // the block holds earlier rows
+  const float s_old = kept ? *sc : 0.f;
+
+  Load16<T> x[NU];
+  uint32_t mx = 0;
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int v = threadIdx.x + i * kThreadsW;
+    if (v < units) x[i].load(src + (size_t)(v / upr) * rstr + (v % upr) * 16);
+    else x[i].zero();
+  }
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float2 f = x[i].pair(e);
+      mx = max(mx, max(finite_abs_bits(f.x), finite_abs_bits(f.y)));
+    }
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+  __syncthreads();  // also: every thread has read the old scale
+#pragma unroll
+  for (int w = 0; w < kThreadsW / 32; ++w) mx = max(mx, s_max[w]);
+  float s = exp2_int(kv8_scale_exp(mx));
+  if (kept) s = fmaxf(s, s_old);
+  const float inv = 1.f / s;               // exact: s is a power of two
+#pragma unroll
+  for (int i = 0; i < NU; ++i) {
+    const int v = threadIdx.x + i * kThreadsW;
+    if (v < units) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = x[i].pair(2 * e), g = x[i].pair(2 * e + 1);
+        w[e] = (uint32_t)f32x2_to_e4m3x2(f.x * inv, f.y * inv) | ((uint32_t)f32x2_to_e4m3x2(g.x * inv, g.y * inv) << 16);
+      }
+      *reinterpret_cast<uint4*>(codes + (size_t)(lo + v / upr) * rstr + (v % upr) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+  if (threadIdx.x == 0 && !(kept && s == s_old)) *sc = s;
+  if (kept && s > s_old) {                 // the earlier rows move to the larger scale
+    const float r = s_old * inv;
+    const int old_units = (lo - first) * upr;
+    for (int v = threadIdx.x; v < old_units; v += kThreadsW) {
+      uint4* at = reinterpret_cast<uint4*>(codes + (size_t)(first + v / upr) * rstr + (v % upr) * 16);
+      uint4 q = *at;
+      uint32_t* w = reinterpret_cast<uint32_t*>(&q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = e4m3x2_to_f32x2((uint16_t)w[e]), g = e4m3x2_to_f32x2((uint16_t)(w[e] >> 16));
+        w[e] = (uint32_t)f32x2_to_e4m3x2(f.x * r, f.y * r) | ((uint32_t)f32x2_to_e4m3x2(g.x * r, g.y * r) << 16);
+      }
+      *at = q;
+    }
+  }
+}
+
+struct ReadParams {
+  const uint8_t* K8;
+  const uint8_t* V8;
+  const float* ks;
+  const float* vs;
+  const int32_t* start;   // [B] or null (0)
+  const int32_t* idx;     // [B][T] or null
+  const int32_t* count;   // [B] or null
+  void* K;                // [B][T][Hkv][d]
+  void* V;
+  void* ws_header;
+  int B, T, n_max, Hkv, d, bshift, nblk, tpc;
+};
+
+// A CTA takes tpc rows of one sequence; its units of 16 codes run over (row, K or V, head,
+// part of d), so neighbouring threads read and write neighbouring bytes.
+template <typename T>
+__global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p) {
+  pdl_enter();
+  const int ctas = (p.T + p.tpc - 1) / p.tpc;  // per sequence
+  const int b = blockIdx.x / ctas;
+  const int t0 = (blockIdx.x - b * ctas) * p.tpc;
+  const int cnt = p.count ? min(p.count[b], p.T) : p.T;
+  const int nrow = min(p.tpc, cnt - t0);
+  if (nrow <= 0) return;
+  const int upr = p.Hkv * p.d / 16;            // units of one row of K (or V)
+  const int uph = p.d / 16;
+  const long long s0 = p.start ? p.start[b] : 0;
+  for (int u0 = threadIdx.x; u0 < nrow * 2 * upr; u0 += 4 * blockDim.x) {
+    uint4 c[4];
+    float s[4];
+    size_t dst[4];
+    bool ok[4], isv[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int u = u0 + i * blockDim.x;
+      ok[i] = u < nrow * 2 * upr;
+      if (!ok[i]) continue;
+      const int r = u / (2 * upr);
+      int w = u - r * 2 * upr;
+      isv[i] = w >= upr;
+      if (isv[i]) w -= upr;
+      const int t = t0 + r;
+      const long long tok = p.idx ? p.idx[(size_t)b * p.T + t] : s0 + t;
+      const bool in = tok >= 0 && tok < p.n_max;
+      dst[i] = ((size_t)b * p.T + t) * p.Hkv * p.d + (size_t)w * 16;
+      c[i] = make_uint4(0u, 0u, 0u, 0u);
+      s[i] = 0.f;
+      if (in) {
+        const size_t row = (size_t)b * p.n_max + (size_t)tok;
+        c[i] = ld_stream_v4((isv[i] ? p.V8 : p.K8) + row * p.Hkv * p.d + (size_t)w * 16);
+        s[i] = __ldg((isv[i] ? p.vs : p.ks) + ((size_t)b * p.nblk + (size_t)(tok >> p.bshift)) * p.Hkv + w / uph);
+      } else if (w == 0 && !isv[i]) {
+        record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)t);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (!ok[i]) continue;
+      const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+      T* out = static_cast<T*>(isv[i] ? p.V : p.K) + dst[i];
+      float f[16];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float2 x = e4m3x2_to_f32x2((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
+        f[2 * e] = x.x * s[i];
+        f[2 * e + 1] = x.y * s[i];
+      }
+      if constexpr (sizeof(T) == 2) {
+        uint4* o = reinterpret_cast<uint4*>(out);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          o[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
+                            pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+      } else {
+        float4* o = reinterpret_cast<float4*>(out);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+      }
+    }
+  }
+}
+
+int log2_of(int x) {
+  int s = 0;
+  while ((1 << s) < x) ++s;
+  return s;
+}
+
+template <typename T>
+cudaError_t launch_write(const WriteParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)(2LL * p.Hkv * p.jmax * p.B));
+  const int nu = (std::min(p.T, p.block) * (p.d / 16) + kThreadsW - 1) / kThreadsW;  // <= 4: 128 x 128
+  if (nu <= 1) return launch_pdl(kv8_write_kernel<T, 1>, grid, dim3(kThreadsW), 0, s, p);
+  if (nu <= 2) return launch_pdl(kv8_write_kernel<T, 2>, grid, dim3(kThreadsW), 0, s, p);
+  return launch_pdl(kv8_write_kernel<T, 4>, grid, dim3(kThreadsW), 0, s, p);
+}
+
+}  // namespace
+
+// blocks that T rows can touch
+static long long write_jmax(int T, int block) { return ((long long)T + block - 2) / block + 1; }
+
+bool kv8_write_grid_ok(const clsa_kv8_cache* c, int T) {
+  return 2LL * c->Hkv * write_jmax(T, c->block) * c->B <= 0x7fffffffLL;
+}
+
+cudaError_t launch_kv8_write(const clsa_kv8_cache* c, const void* K, const void* V, const int32_t* start,
+                             const int32_t* count, int T, clsa_dtype dt, void* ws_header, cudaStream_t s) {
+  WriteParams p{};
+  p.K = K;
+  p.V = V;
+  p.start = start;
+  p.count = count;
+  p.K8 = static_cast<uint8_t*>(c->K8);
+  p.V8 = static_cast<uint8_t*>(c->V8);
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.ws_header = ws_header;
+  p.B = c->B;
+  p.T = T;
+  p.n_max = c->n_max;
+  p.Hkv = c->Hkv;
+  p.d = c->d;
+  p.block = c->block;
+  p.nblk = (c->n_max + c->block - 1) / c->block;
+  p.jmax = (int)write_jmax(T, c->block);
+  const cudaError_t e = dt == CLSA_BF16 ? launch_write<__nv_bfloat16>(p, s) : launch_write<float>(p, s);
+  launches_add(1, s);
+  return e;
+}
+
+// rows a CTA takes: about 4 units a thread
+static int read_tpc(const clsa_kv8_cache* c) { return std::max(1, 1024 / (2 * c->Hkv * c->d / 16)); }
+
+bool kv8_read_grid_ok(const clsa_kv8_cache* c, int T) {
+  const int tpc = read_tpc(c);
+  return ((long long)T + tpc - 1) / tpc * c->B <= 0x7fffffffLL && 2LL * tpc * c->Hkv * c->d / 16 < (1LL << 30);
+}
+
+cudaError_t launch_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const int32_t* idx, const int32_t* count,
+                            int T, clsa_dtype dt, void* K, void* V, void* ws_header, cudaStream_t s) {
+  ReadParams p{};
+  p.K8 = static_cast<const uint8_t*>(c->K8);
+  p.V8 = static_cast<const uint8_t*>(c->V8);
+  p.ks = c->k_scale;
+  p.vs = c->v_scale;
+  p.start = start;
+  p.idx = idx;
+  p.count = count;
+  p.K = K;
+  p.V = V;
+  p.ws_header = ws_header;
+  p.B = c->B;
+  p.T = T;
+  p.n_max = c->n_max;
+  p.Hkv = c->Hkv;
+  p.d = c->d;
+  p.bshift = log2_of(c->block);
+  p.nblk = (c->n_max + c->block - 1) / c->block;
+  p.tpc = read_tpc(c);
+  const dim3 grid((unsigned)(((long long)T + p.tpc - 1) / p.tpc * c->B));
+  const cudaError_t e = dt == CLSA_BF16 ? launch_pdl(kv8_read_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p)
+                                        : launch_pdl(kv8_read_kernel<float>, grid, dim3(256), 0, s, p);
+  launches_add(1, s);
+  return e;
+}
+
+}  // namespace clsa

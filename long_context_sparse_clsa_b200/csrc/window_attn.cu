@@ -1,0 +1,68 @@
+// Attention with a sliding window and sink tokens.
+#include "stream_attn.cuh"
+
+namespace clsa {
+
+namespace {
+
+stream::Params params_of(const clsa_window_args* a, float scale) {
+  stream::Params p{};
+  p.Q = a->Q;
+  p.K = a->K;
+  p.V = a->V;
+  p.count = a->seq_lens;
+  p.O = a->O;
+  p.lse = a->lse;
+  p.q_sl = (long long)a->Hq * a->d;
+  p.q_sb = (long long)a->T * a->Hq * a->d;
+  p.B = a->B;
+  p.Hkv = a->Hkv;
+  p.G = a->Hq / a->Hkv;
+  p.R = a->T * p.G;
+  p.n_max = a->n_max;
+  p.seqs = a->B;
+  p.T = a->T;
+  p.window = std::min(a->window, a->n_max);
+  p.sinks = std::min(a->sinks, a->n_max);
+  p.scale_log2 = scale * 1.4426950408889634f;
+  const int rows = 8 * stream::row_tiles(p.R, a->dtype == CLSA_F32);
+  p.nrg = (p.R + rows - 1) / rows;
+  return p;
+}
+
+// calls f<CACHE, F32, D, NT>
+template <typename F>
+auto dispatch(const clsa_window_args* a, int R, F&& f) {
+  const bool d128 = a->d == 128;
+  if (a->dtype == CLSA_F32)
+    return d128 ? f.template operator()<stream::kFp32, true, 128, 1>() : f.template operator()<stream::kFp32, true, 64, 1>();
+  if (stream::row_tiles(R, false) == 1)
+    return d128 ? f.template operator()<stream::kBf16, false, 128, 1>() : f.template operator()<stream::kBf16, false, 64, 1>();
+  return d128 ? f.template operator()<stream::kBf16, false, 128, 2>() : f.template operator()<stream::kBf16, false, 64, 2>();
+}
+
+struct Bytes {
+  const stream::Params& p;
+  template <int C, bool F32, int D, int NT> size_t operator()() const { return stream::ws_bytes<C, F32, D, NT>(p); }
+};
+struct Launch {
+  const stream::Params& p;
+  void* ws;
+  cudaStream_t s;
+  template <int C, bool F32, int D, int NT> cudaError_t operator()() const { return stream::launch<C, F32, D, NT>(p, ws, s); }
+};
+
+}  // namespace
+
+size_t window_attn_ws_bytes(const clsa_window_args* a) {
+  const stream::Params p = params_of(a, 1.f);
+  return dispatch(a, p.R, Bytes{p});
+}
+
+cudaError_t launch_window_attn(const clsa_window_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s) {
+  stream::Params p = params_of(a, scale);
+  p.ws_header = ws_header;
+  return dispatch(a, p.R, Launch{p, ws_body, s});
+}
+
+}  // namespace clsa
