@@ -125,6 +125,10 @@ cudaError_t launch_kv8_attn(const clsa_kv8_attn_args* a, float scale, void* ws_h
 size_t window_attn_ws_bytes(const clsa_window_args* a);
 cudaError_t launch_window_attn(const clsa_window_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s);
 
+// rows of a chunk on tcgen05 (bf16)
+bool window_tc_supported(const clsa_window_args* a);
+cudaError_t launch_window_tc(const clsa_window_args* a, float scale, void* ws_header, cudaStream_t s);
+
 // ----- failure-detection self-test (a wait that runs out and reports) ------------
 cudaError_t launch_selftest_timeout(int which, void* ws_header, void* ws_body, cudaStream_t s);
 

@@ -52,14 +52,23 @@ struct Launch {
   template <int C, bool F32, int D, int NT> cudaError_t operator()() const { return stream::launch<C, F32, D, NT>(p, ws, s); }
 };
 
+// chunks with more rows per KV head than this run in row tiles of 128 on tcgen05
+constexpr long long kStreamRows = 64;
+
+bool use_tc(const clsa_window_args* a) {
+  return (long long)a->T * (a->Hq / a->Hkv) > kStreamRows && window_tc_supported(a);
+}
+
 }  // namespace
 
 size_t window_attn_ws_bytes(const clsa_window_args* a) {
+  if (use_tc(a)) return 0;
   const stream::Params p = params_of(a, 1.f);
   return dispatch(a, p.R, Bytes{p});
 }
 
 cudaError_t launch_window_attn(const clsa_window_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s) {
+  if (use_tc(a)) return launch_window_tc(a, scale, ws_header, s);
   stream::Params p = params_of(a, scale);
   p.ws_header = ws_header;
   return dispatch(a, p.R, Launch{p, ws_body, s});
