@@ -203,6 +203,7 @@ class Workspace:
     def __init__(self, nbytes: int, device=None):
         self.nbytes = max(int(nbytes), 256)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        self.addr = self.buf.data_ptr()
         _check(load_library().clsa_workspace_init(_p(self.buf), self.nbytes, _stream()), "workspace_init")
 
     @property
@@ -441,19 +442,36 @@ def prefill_attention(q_idx, k_idx, K, V, Q, k, idx, count, mode: int = 0, scale
 
 # ---------------------------------------------------------------------------- positions, 8-bit cache
 
-def _here(t: Optional[torch.Tensor], what: str, shape=None, dtype=None):
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _now(t: torch.Tensor, what: str):
+    """(current device, its current stream's handle), what a call runs on; t: its first tensor."""
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
+    dev = torch.cuda.current_device()
+    return dev, _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _here(t: Optional[torch.Tensor], dev: int, what: str, shape=None, dtype=None):
     """The address of a contiguous tensor on the current device, of the given shape and dtype."""
     if t is None:
         return None
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != dev or not t.is_contiguous():
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what}: a contiguous CUDA tensor is wanted")
+        raise ValueError(f"{what} is on {t.device}, the current device is cuda:{dev}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{what}: {dtype} is wanted, got {t.dtype}")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{what}: shape {tuple(shape)} is wanted, got {tuple(t.shape)}")
     return t.data_ptr()
+
+
+def _ws(ws: Workspace, dev: int) -> int:
+    if ws.buf.get_device() != dev:
+        raise ValueError(f"the workspace is on {ws.buf.device}, the current device is cuda:{dev}")
+    return ws.addr
 
 
 _ROPE_LAYOUT = {"half": 0, "interleaved": 1}
@@ -479,12 +497,14 @@ def rope(q, k, pos, rot: Optional[int] = None, layout: str = "half", theta: floa
     Hq, Hk = (q.shape[-2] if q is not None else 0), (k.shape[-2] if k is not None else 0)
     if k is not None and k.shape[-1] != d:
         raise ValueError(f"k: head dimension {d} is wanted, got {k.shape[-1]}")
+    dev, stream = _now(x, "q" if q is not None else "k")
     a = RopeArgs(_dt(x), q.numel() // (Hq * d) if Hq else 0, k.numel() // (Hk * d) if Hk else 0, n_pos, Hq, Hk, d,
                  d if rot is None else rot, _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], bool(inverse), orig_len,
-                 theta, factor, beta_fast, beta_slow, mscale, _here(q, "q", None, dt), _here(k, "k", None, dt),
-                 _here(pos, "pos", None, torch.int32), _here(q_out, "q_out", q.shape if q is not None else None, dt),
-                 _here(k_out, "k_out", k.shape if k is not None else None, dt))
-    _check(load_library().clsa_rope(ctypes.byref(a), _stream()), "clsa_rope")
+                 theta, factor, beta_fast, beta_slow, mscale, _here(q, dev, "q", None, dt), _here(k, dev, "k", None, dt),
+                 _here(pos, dev, "pos", None, torch.int32),
+                 _here(q_out, dev, "q_out", q.shape if q is not None else None, dt),
+                 _here(k_out, dev, "k_out", k.shape if k is not None else None, dt))
+    _check(load_library().clsa_rope(ctypes.byref(a), stream), "clsa_rope")
     return q_out, k_out
 
 
@@ -499,9 +519,12 @@ class Kv8Cache:
         self.block = int(block)
         self.K8, self.V8, self.k_scale, self.v_scale = K8, V8, k_scale, v_scale
         scales = (self.B, -(-self.n_max // max(self.block, 1)), self.Hkv)
-        self.args = Kv8CacheArgs(self.B, self.n_max, self.Hkv, self.d, self.block, _here(K8, "K8"),
-                                 _here(V8, "V8", K8.shape, K8.dtype), _here(k_scale, "k_scale", scales, torch.float32),
-                                 _here(v_scale, "v_scale", scales, torch.float32))
+        if not K8.is_cuda:
+            raise ValueError("K8: a contiguous CUDA tensor is wanted")
+        self.device = dev = K8.get_device()
+        self.args = Kv8CacheArgs(self.B, self.n_max, self.Hkv, self.d, self.block, _here(K8, dev, "K8"),
+                                 _here(V8, dev, "V8", K8.shape, K8.dtype), _here(k_scale, dev, "k_scale", scales, torch.float32),
+                                 _here(v_scale, dev, "v_scale", scales, torch.float32))
         self._ref = ctypes.byref(self.args)
 
     @classmethod
@@ -513,15 +536,24 @@ class Kv8Cache:
         return cls(*codes, *scales, block)
 
 
+def _on(cache: "Kv8Cache"):
+    """_now(), where the cache is on the current device."""
+    dev, stream = _now(cache.K8, "cache")
+    if cache.device != dev:
+        raise ValueError(f"the cache is on cuda:{cache.device}, the current device is cuda:{dev}")
+    return dev, stream
+
+
 def kv8_write(cache: Kv8Cache, K, V, start, count=None, ws: Optional[Workspace] = None) -> Kv8Cache:
     """Quantise K, V [B][T][Hkv][d] into the cache as tokens start[b] + t, t < count[b] (see clsa.h)."""
     lib = load_library()
     T = K.shape[1]
     shape = (cache.B, T, cache.Hkv, cache.d)
     ws = ws or Workspace(lib.clsa_kv8_workspace_size(), K.device)
-    _check(lib.clsa_kv8_write(cache._ref, _here(K, "K", shape), _here(V, "V", shape, K.dtype),
-                              _here(start, "start", (cache.B,), torch.int32),
-                              _here(count, "count", (cache.B,), torch.int32), T, _dt(K), ws.ptr, ws.nbytes, _stream()),
+    dev, stream = _on(cache)
+    _check(lib.clsa_kv8_write(cache._ref, _here(K, dev, "K", shape), _here(V, dev, "V", shape, K.dtype),
+                              _here(start, dev, "start", (cache.B,), torch.int32),
+                              _here(count, dev, "count", (cache.B,), torch.int32), T, _dt(K), _ws(ws, dev), ws.nbytes, stream),
            "clsa_kv8_write")
     return cache
 
@@ -541,22 +573,23 @@ def kv8_read(cache: Kv8Cache, K=None, V=None, start=None, idx=None, count=None, 
     T = K.shape[1]
     shape = (cache.B, T, cache.Hkv, cache.d)
     ws = ws or Workspace(lib.clsa_kv8_workspace_size(), K.device)
-    _check(lib.clsa_kv8_read(cache._ref, _here(start, "start", (cache.B,), torch.int32),
-                             _here(idx, "idx", (cache.B, T), torch.int32),
-                             _here(count, "count", (cache.B,), torch.int32), T, _dt(K), _here(K, "K", shape),
-                             _here(V, "V", shape, K.dtype), ws.ptr, ws.nbytes, _stream()), "clsa_kv8_read")
+    dev, stream = _on(cache)
+    _check(lib.clsa_kv8_read(cache._ref, _here(start, dev, "start", (cache.B,), torch.int32),
+                             _here(idx, dev, "idx", (cache.B, T), torch.int32),
+                             _here(count, dev, "count", (cache.B,), torch.int32), T, _dt(K), _here(K, dev, "K", shape),
+                             _here(V, dev, "V", shape, K.dtype), _ws(ws, dev), ws.nbytes, stream), "clsa_kv8_read")
     return K, V
 
 
-def _kv8_attn_args(Q, cache, count, idx, scale, O, lse) -> Kv8AttnArgs:
+def _kv8_attn_args(dev, Q, cache, count, idx, scale, O, lse) -> Kv8AttnArgs:
     L, B, Hq, d = Q.shape
     if d != cache.d:
         raise ValueError(f"Q: head dimension {cache.d} is wanted, got {d}")
     if idx is not None and (idx.dim() != 2 or idx.shape[0] != B):
         raise ValueError(f"idx: shape [{B}][k] is wanted, got {tuple(idx.shape)}")
-    return Kv8AttnArgs(_dt(Q), B, L, Hq, idx.shape[1] if idx is not None else 0, scale, cache.args, _here(Q, "Q"),
-                       _here(idx, "idx", None, torch.int32), _here(count, "count", (B,), torch.int32),
-                       _here(O, "O", Q.shape, Q.dtype), _here(lse, "lse", (L, B, Hq), torch.float32))
+    return Kv8AttnArgs(_dt(Q), B, L, Hq, idx.shape[1] if idx is not None else 0, scale, cache.args, _here(Q, dev, "Q"),
+                       _here(idx, dev, "idx", None, torch.int32), _here(count, dev, "count", (B,), torch.int32),
+                       _here(O, dev, "O", Q.shape, Q.dtype), _here(lse, dev, "lse", (L, B, Hq), torch.float32))
 
 
 def _need(size: int, where: str) -> int:
@@ -568,7 +601,7 @@ def _need(size: int, where: str) -> int:
 def kv8_attn_workspace_size(Q, cache: Kv8Cache, idx=None) -> int:
     """Workspace bytes of kv8_attn for these tensors (Q [L][B][Hq][d] or [B][Hq][d])."""
     Qv = Q.unsqueeze(0) if Q.dim() == 3 else Q
-    a = _kv8_attn_args(Qv, cache, None, idx, 0.0, Qv, None)
+    a = _kv8_attn_args(_on(cache)[0], Qv, cache, None, idx, 0.0, Qv, None)
     a.count = a.Q  # any aligned address: the size does not read it
     return _need(load_library().clsa_kv8_attn_workspace_size(ctypes.byref(a)), "clsa_kv8_attn_workspace_size")
 
@@ -586,27 +619,28 @@ def kv8_attn(Q, cache: Kv8Cache, count, idx=None, scale: float = 0.0, ws: Option
         O = torch.empty_like(Q)
     if lse is None and want_lse:
         lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
-    a = _kv8_attn_args(Q, cache, count, idx, scale, O, lse)
+    dev, stream = _on(cache)
+    a = _kv8_attn_args(dev, Q, cache, count, idx, scale, O, lse)
     ref = ctypes.byref(a)
     if ws is None:
         ws = Workspace(_need(lib.clsa_kv8_attn_workspace_size(ref), "clsa_kv8_attn_workspace_size"), Q.device)
-    _check(lib.clsa_kv8_attn(ref, ws.ptr, ws.nbytes, _stream()), "clsa_kv8_attn")
+    _check(lib.clsa_kv8_attn(ref, _ws(ws, dev), ws.nbytes, stream), "clsa_kv8_attn")
     return (O[0], lse[0] if lse is not None else None) if squeeze else (O, lse)
 
 
-def _window_args(Q, K, V, seq_lens, window, sinks, scale, O, lse) -> WindowArgs:
+def _window_args(dev, Q, K, V, seq_lens, window, sinks, scale, O, lse) -> WindowArgs:
     B, T, Hq, d = Q.shape
     n_max, Hkv = K.shape[1], K.shape[2]
     shape = (B, n_max, Hkv, d)
-    return WindowArgs(_dt(Q), B, T, n_max, Hq, Hkv, d, window, sinks, scale, _here(Q, "Q"),
-                      _here(K, "K", shape, Q.dtype), _here(V, "V", shape, Q.dtype),
-                      _here(seq_lens, "seq_lens", (B,), torch.int32), _here(O, "O", Q.shape, Q.dtype),
-                      _here(lse, "lse", (B, T, Hq), torch.float32))
+    return WindowArgs(_dt(Q), B, T, n_max, Hq, Hkv, d, window, sinks, scale, _here(Q, dev, "Q"),
+                      _here(K, dev, "K", shape, Q.dtype), _here(V, dev, "V", shape, Q.dtype),
+                      _here(seq_lens, dev, "seq_lens", (B,), torch.int32), _here(O, dev, "O", Q.shape, Q.dtype),
+                      _here(lse, dev, "lse", (B, T, Hq), torch.float32))
 
 
 def window_attn_workspace_size(Q, K, window: int, sinks: int = 0) -> int:
     """Workspace bytes of window_attn for these tensors."""
-    a = _window_args(Q, K, K, None, window, sinks, 0.0, Q, None)
+    a = _window_args(_now(Q, "Q")[0], Q, K, K, None, window, sinks, 0.0, Q, None)
     a.seq_lens = a.Q  # any aligned address: the size does not read it
     return _need(load_library().clsa_window_attn_workspace_size(ctypes.byref(a)), "clsa_window_attn_workspace_size")
 
@@ -620,11 +654,12 @@ def window_attn(Q, K, V, seq_lens, window: int, sinks: int = 0, scale: float = 0
         O = torch.empty_like(Q)
     if lse is None and want_lse:
         lse = torch.empty(Q.shape[:3], dtype=torch.float32, device=Q.device)
-    a = _window_args(Q, K, V, seq_lens, window, sinks, scale, O, lse)
+    dev, stream = _now(Q, "Q")
+    a = _window_args(dev, Q, K, V, seq_lens, window, sinks, scale, O, lse)
     ref = ctypes.byref(a)
     if ws is None:
         ws = Workspace(_need(lib.clsa_window_attn_workspace_size(ref), "clsa_window_attn_workspace_size"), Q.device)
-    _check(lib.clsa_window_attn(ref, ws.ptr, ws.nbytes, _stream()), "clsa_window_attn")
+    _check(lib.clsa_window_attn(ref, _ws(ws, dev), ws.nbytes, stream), "clsa_window_attn")
     return O, lse
 
 
