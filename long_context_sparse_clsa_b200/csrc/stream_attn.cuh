@@ -44,10 +44,9 @@
 namespace clsa {
 namespace stream {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                   // tokens of a tile
-constexpr int kMinTiles = 2 * kWarps;       // fewest tiles worth a CTA
+constexpr int kMinTiles = 4;                // fewest tiles worth a CTA
+constexpr int kAhead = 4;                   // tiles of a warp between its L2 prefetch and its loads
 constexpr float kNone = -3e38f;             // reference of a row that has seen nothing
 constexpr float kTau = 8.f;
 constexpr float kLift = 7.f;                // 8-bit cache: the largest p of a row lies in [2^7, 2^15] of half range
@@ -144,10 +143,15 @@ __device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
 template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
 
+// warps of a CTA (one CTA per SM): what the registers allow, 168 or 255 a thread.  One large CTA
+// rather than three small: a unit that all SMs share has a third of the partials to merge.
+template <int CACHE, int NT>
+__host__ __device__ constexpr int warps_of() { return NT == 1 && CACHE != kFp32 ? 12 : 8; }
+
 // shared memory: the warps' outputs, or the weights of up to P contributors
-template <int D, int NT>
+template <int CACHE, int D, int NT>
 __host__ __device__ constexpr size_t smem_bytes(int P) {
-  const size_t o = (size_t)kWarps * NT * 8 * D * 4, w = (size_t)P * NT * 8 * 4;
+  const size_t o = (size_t)warps_of<CACHE, NT>() * NT * 8 * D * 4, w = (size_t)P * NT * 8 * 4;
   return o > w ? o : w;
 }
 
@@ -155,6 +159,7 @@ template <int CACHE, bool F32, int D, int NT>
 __device__ void kernel_body(const Params& p) {
   static_assert(F32 ? CACHE != kBf16 : CACHE != kFp32, "bf16 cache: bf16 rows; fp32 cache: fp32 rows");
   constexpr bool FP8 = CACHE == kE4m3;
+  constexpr int kWarps = warps_of<CACHE, NT>(), kThreads = kWarps * 32;
   constexpr int ROWS = NT * 8;
   constexpr int ES = FP8 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
   constexpr int KC = D * ES / 64;              // 16-byte chunks of a token's row that a lane takes
@@ -376,13 +381,25 @@ __device__ void kernel_body(const Params& p) {
     };
     auto load_scale = [&](int tok) { return FP8 && tok >= 0 ? __ldg(scp + (size_t)(tok >> p.bshift) * p.Hkv) : 1.f; };
 
+    // the tokens' lines of tile t on their way into L2 (a lane per row; selections are small)
+    auto ahead = [&](int t) {
+      const int i = t * kTile + (lane & 15);
+      if ((FP8 && p.idx) || t >= t_end || i >= it.npos) return;
+      const uint8_t* a = (lane < 16 ? kb : vb) + (size_t)(i < it.keep ? i : i + it.shift) * rstr;
+#pragma unroll
+      for (int x = 0; x < (D * ES + 127) / 128; ++x) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 128 * x));
+    };
+
     int t = t_beg + warp;
+#pragma unroll
+    for (int x = 1; x < kAhead; ++x) ahead(t + x * kWarps);
     int tok = token(t), tok_n = token(t + kWarps);
     float sc = load_scale(tok);
     load_k(tok);
     load_v(tok);
     for (; t < t_end; t += kWarps) {
       const int tok_nn = token(t + 2 * kWarps);
+      ahead(t + kAhead * kWarps);
       // S^T
       float sa[NT][4];
 #pragma unroll
@@ -643,7 +660,7 @@ __device__ void kernel_body(const Params& p) {
       __syncthreads();  // shared memory is free again
     } else {
       // slot 0 of a CTA: the unit began before it; slot 1: the unit began here and goes on behind it
-      const auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc * N / P > ts ? 0 : 1)) * slot_floats<D, NT>(); };
+      const auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats<D, NT>(); };
       float* my = slot(c);
       for (int i = tid; i < ROWS * (D / 4); i += kThreads) __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i));
       if (tid < ROWS) {
@@ -685,12 +702,13 @@ __device__ void kernel_body(const Params& p) {
         for (int i = tid; i < nr * (D / 4); i += kThreads) {
           const int row = i / (D / 4);
           float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int j0 = 0; j0 < n; j0 += 8) {
-            float4 y[8];
+          constexpr int kB = 16;  // loads in flight
+          for (int j0 = 0; j0 < n; j0 += kB) {
+            float4 y[kB];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + min(j0 + j, n - 1))) + i);
+            for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + min(j0 + j, n - 1))) + i);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < kB; ++j) {
               const float w = j0 + j < n ? sm_o[(j0 + j) * ROWS + row] : 0.f;
               if (j0 + j < n) {
                 x.x = fmaf(w, y[j].x, x.x);
@@ -712,12 +730,8 @@ __device__ void kernel_body(const Params& p) {
   }
 }
 
-// CTAs of a launch: blocks per SM that the kernel's registers allow
-template <int CACHE, int NT>
-constexpr int blocks_per_sm() { return NT == 1 && CACHE != kFp32 ? 3 : 2; }
-
 template <int CACHE, bool F32, int D, int NT>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm<CACHE, NT>()) stream_attn_kernel(const Params p) {
+__global__ void __launch_bounds__(warps_of<CACHE, NT>() * 32, 1) stream_attn_kernel(const Params p) {
   pdl_enter();
   kernel_body<CACHE, F32, D, NT>(p);
 }
@@ -729,19 +743,19 @@ inline int row_tiles(int R, bool f32) { return R <= 8 || f32 ? 1 : 2; }
 
 template <int CACHE, bool F32, int D, int NT>
 size_t ws_bytes(const Params& p) {
-  const int P = std::max(1, device_info().sm_count) * blocks_per_sm<CACHE, NT>();
+  const int P = std::max(1, device_info().sm_count);
   return counter_bytes(p) + (size_t)2 * P * slot_floats<D, NT>() * 4;
 }
 
 template <int CACHE, bool F32, int D, int NT>
 cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
-  const int P = std::max(1, device_info().sm_count) * blocks_per_sm<CACHE, NT>();
+  const int P = std::max(1, device_info().sm_count);
   p.counter = static_cast<uint32_t*>(ws_body);
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
-  const size_t smem = smem_bytes<D, NT>(P);
+  const size_t smem = smem_bytes<CACHE, D, NT>(P);
   auto* k = stream_attn_kernel<CACHE, F32, D, NT>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3(P), dim3(kThreads), smem, s, p);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3(P), dim3(warps_of<CACHE, NT>() * 32), smem, s, p);
   launches_add(1, s);
   return e;
 }

@@ -130,6 +130,24 @@ __device__ __forceinline__ void st_32x32b_x8(uint32_t taddr, const uint32_t (&r)
                : "memory");
 }
 
+// pairs of floats: two products or sums an instruction
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f32x2_get(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_constant__ Maps maps, const WParams p) {
   using S = Smem<D>;
@@ -142,9 +160,9 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   uint64_t* q_full = bars + 16;              // [2]
   uint64_t* q_empty = bars + 18;
   uint64_t* s_full = bars + 20;
-  uint64_t* p_full = bars + 22;
-  uint64_t* o_full = bars + 24;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  uint64_t* p_full = bars + 22;              // [2][2]: the halves of P
+  uint64_t* o_full = bars + 26;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -160,7 +178,8 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       mbar_init(q_full + i, 1);
       mbar_init(q_empty + i, 1);
       mbar_init(s_full + i, 1);
-      mbar_init(p_full + i, 4);  // one arrival per softmax warp
+      mbar_init(p_full + 2 * i, 4);  // one arrival per softmax warp
+      mbar_init(p_full + 2 * i + 1, 4);
       mbar_init(o_full + i, 1);
     }
     fence_mbar_init();
@@ -301,17 +320,22 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (t < w.ntile) {
-          ok = wait(p_full + t, np[t]++ & 1u, 65);
-          if (!ok) break;
-          tc::fence_after_sync();
-          if (lane == 0) {
-            const uint32_t va = smem_u32(base + S::ring + vslot * S::tile);
+          const uint32_t va = smem_u32(base + S::ring + vslot * S::tile);
 #pragma unroll
-            for (int ks = 0; ks < kTok / 16; ++ks)
-              mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, tc::sw128_desc_mn(va + ks * 16 * 128, kAtom), idesc_pv,
-                          j > 0 || ks > 0);
-            if (j == w.nkv - 1) tc::mma_commit(o_full + t);
+          for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(p_full + 2 * t + h, np[t] & 1u, 65);
+            if (!ok) break;
+            tc::fence_after_sync();
+            if (lane == 0) {
+#pragma unroll
+              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+                mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, tc::sw128_desc_mn(va + ks * 16 * 128, kAtom), idesc_pv,
+                            j > 0 || ks > 0);
+              if (h == 1 && j == w.nkv - 1) tc::mma_commit(o_full + t);
+            }
           }
+          if (!ok) break;
+          ++np[t];
           __syncwarp();
         }
         if (more && t < nw.ntile) {
@@ -373,10 +397,15 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
           for (int c = 0; c < kTok; ++c)
             if (!(c < cs || (c >= cl && c <= ch))) v[c] = 0xff800000u;
         }
-        float mx = kNone;
+        float x0 = kNone, x1 = kNone, x2 = kNone, x3 = kNone;
 #pragma unroll
-        for (int c = 0; c < kTok; c += 2) mx = fmaxf(mx, fmaxf(__uint_as_float(v[c]), __uint_as_float(v[c + 1])));
-        mx *= p.scale_log2;                         // scale > 0: the maximum commutes
+        for (int c = 0; c < kTok; c += 8) {
+          x0 = fmaxf(fmaxf(x0, __uint_as_float(v[c])), __uint_as_float(v[c + 1]));
+          x1 = fmaxf(fmaxf(x1, __uint_as_float(v[c + 2])), __uint_as_float(v[c + 3]));
+          x2 = fmaxf(fmaxf(x2, __uint_as_float(v[c + 4])), __uint_as_float(v[c + 5]));
+          x3 = fmaxf(fmaxf(x3, __uint_as_float(v[c + 6])), __uint_as_float(v[c + 7]));
+        }
+        const float mx = fmaxf(fmaxf(x0, x1), fmaxf(x2, x3)) * p.scale_log2;  // scale > 0: the maximum commutes
         const bool up = mx > m + kTau;
         if (__any_sync(0xffffffffu, up)) {          // P V of the token tile before has completed
           const float mn = up ? mx : m;
@@ -395,25 +424,36 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
           l *= f;
           m = mn;
         }
-        float s0 = 0.f, s1 = 0.f;
+        uint64_t s0 = 0, s1 = 0;                    // pairs of sums
+        const uint64_t sc2 = f32x2(p.scale_log2, p.scale_log2), nm2 = f32x2(-m, -m);
 #pragma unroll
         for (int h = 0; h < 8; ++h) {               // 16 columns at a time: few registers beside the scores
           uint32_t pw[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            const float a = fast_exp2(fmaf(__uint_as_float(v[16 * h + 2 * c]), p.scale_log2, -m));
-            const float b = fast_exp2(fmaf(__uint_as_float(v[16 * h + 2 * c + 1]), p.scale_log2, -m));
-            s0 += a;
-            s1 += b;
+            float a, b;
+            f32x2_get(fma_f32x2(f32x2(__uint_as_float(v[16 * h + 2 * c]), __uint_as_float(v[16 * h + 2 * c + 1])), sc2, nm2), a, b);
+            a = fast_exp2(a);
+            b = fast_exp2(b);
+            if (c & 1) s1 = add_f32x2(s1, f32x2(a, b));
+            else s0 = add_f32x2(s0, f32x2(a, b));
             pw[c] = pack_bf16x2(a, b);
           }
           st_32x32b_x8(ts + 8u * h, pw);
+          if (h == 3) {                             // the first half of P: its MMAs may start
+            tc::st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 2 * t);
+          }
         }
-        l += s0 + s1;
+        float sa, sb;
+        f32x2_get(add_f32x2(s0, s1), sa, sb);
+        l += sa + sb;
         tc::st_wait();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + t);
+        if (lane == 0) mbar_arrive(p_full + 2 * t + 1);
       }
       if (!ok) break;
       uint4* out = reinterpret_cast<uint4*>(p.O + row * D);
