@@ -31,9 +31,10 @@
 // halves it is 2^7 larger still (halves end at 2^16), so that the halves' smallest step, 2^-24,
 // is 2^-31 of the largest.
 //
-// Work split.  All (sequence, row group, KV head) units' tiles form one line; CTA c takes
-// tiles [c N / P, (c + 1) N / P), so ragged lengths balance.  A unit that several CTAs share
-// is merged by the one that arrives last, in CTA order (the result does not depend on who that is).
+// Work split.  A unit is a (sequence, row group, KV head).  Few units of like length get whole CTAs
+// each; else all units' tiles form one line that the CTAs share equally, so ragged lengths
+// balance.  A unit that several CTAs share is merged by the one that arrives last, in CTA
+// order (the result does not depend on who that is).
 #pragma once
 
 #include <algorithm>
@@ -173,40 +174,51 @@ __device__ void kernel_body(const Params& p) {
   extern __shared__ __align__(16) float sm_o[];
   __shared__ float sm_m[3][kWarps][ROWS];
   __shared__ float sm_f[ROWS];
-  __shared__ long long sm_scan[kWarps];
-  __shared__ long long sm_base;
-  __shared__ int sm_item, sm_last;
+  __shared__ long long sm_off[ROWS];           // where the unit's rows lie in Q and O
+  __shared__ int sm_scan[2][kWarps];
+  __shared__ int sm_top[kWarps];
+  __shared__ int sm_unit[4];
+  __shared__ int sm_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
-  const int nS = p.B * p.nrg;
+  const int nS = p.B * p.nrg, c = blockIdx.x;
 
-  // ---- the line of tiles, and this CTA's stretch [r0, r1) of it ----------------------------
+  // ---- the units' tiles, and how the CTAs share them ------------------------------------------
   auto tiles_of = [&](int npos) { return (npos + kTile - 1) / kTile; };
+  // sum of x over the threads, and over those before this one (two in turn: sm_scan has two rows)
+  auto block_scan = [&](int row, int x, int& before) {
+    int v = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int w = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += w;
+    }
+    if (lane == 31) sm_scan[row][warp] = v;
+    __syncthreads();
+    int sum = 0;
+    before = v - x;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm_scan[row][w];
+      sum += sm_scan[row][w];
+    }
+    return sum;
+  };
+  const int nU = nS * p.Hkv;
+  const bool few = nU <= (int)gridDim.x && nU <= kThreads;  // a thread per unit; else a run of items per thread
   const int per = (nS + kThreads - 1) / kThreads;
-  long long mine = 0;
-  for (int s = tid * per; s < min(nS, (tid + 1) * per); ++s)
-    mine += (long long)tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
-  long long scan = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, scan, o);
-    if (lane >= o) scan += v;
+  int mine = 0, before;
+  if (few) {
+    if (tid < nU) mine = tiles_of(item_of(p, tid / p.Hkv, ROWS).npos);
+  } else {
+    for (int s = tid * per; s < min(nS, (tid + 1) * per); ++s) mine += tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
   }
-  if (lane == 31) sm_scan[warp] = scan;
-  __syncthreads();
-  long long N = 0, before = scan - mine;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += sm_scan[w];
-    N += sm_scan[w];
-  }
-  const int P = (int)min((long long)gridDim.x, (N + kMinTiles - 1) / kMinTiles);
-  const int c = blockIdx.x;
+  const int N = block_scan(0, mine, before);
 
   auto out_at = [&](int b, int g, int row) { return (long long)(row / p.G) * p.q_sl + b * p.q_sb + (long long)(g * p.G + row % p.G) * D; };
-  auto store4 = [&](int b, int g, int row, int col, float4 x) {
-    TQ* o = static_cast<TQ*>(p.O) + out_at(b, g, row) + col;
+  auto store4 = [&](long long at, float4 x) {
+    TQ* o = static_cast<TQ*>(p.O) + at;
     if constexpr (F32) *reinterpret_cast<float4*>(o) = x;
     else *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   };
@@ -218,104 +230,96 @@ __device__ void kernel_body(const Params& p) {
     const int nr = min(ROWS, p.R - it.rg * ROWS);
     for (int i = tid; i < p.Hkv * nr * (D / 4); i += kThreads) {
       const int g = i / (nr * (D / 4)), j = i % (nr * (D / 4));
-      const int row = it.rg * ROWS + j / (D / 4);
-      store4(it.b, g, row, (j % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
-      if (p.lse && j % (D / 4) == 0) p.lse[out_at(it.b, g, row) / D] = -INFINITY;
+      const long long at = out_at(it.b, g, it.rg * ROWS + j / (D / 4));
+      store4(at + (j % (D / 4)) * 4, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (p.lse && j % (D / 4) == 0) p.lse[at / D] = -INFINITY;
     }
   }
-  if (c >= P) return;
-  long long r0 = c * N / P;
-  const long long r1 = (c + 1) * N / P;
-  if (mine > 0 && before <= r0 && r0 < before + mine) {  // one thread: its items hold tile r0
-    long long base = before;
-    int s = tid * per;
-    for (;; ++s) {
-      const long long t = (long long)tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
-      if (r0 < base + t) break;
-      base += t;
+  if (N == 0) return;
+
+  // Two ways to share.  Whole CTAs per unit (a unit of x tiles takes x / q of them, q = tiles a CTA):
+  // no CTA works on two units one behind the other, and where a unit has one CTA there is
+  // nothing to merge.  Taken where it leaves no CTA more than an eighth (and two rounds of
+  // its warps) above q; else the line of all tiles is cut into equal stretches.
+  const int q0 = (N + (int)gridDim.x - 1) / (int)gridDim.x;
+  bool whole = few;
+  if (few) {
+    const int want = mine > 0 ? max(1, min(mine / q0, (mine + kMinTiles - 1) / kMinTiles)) : 0;
+    const int load = want > 0 ? (mine + want - 1) / want : 0;
+    const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)load);
+    if (lane == 0) sm_top[warp] = top;
+    int pref;
+    const int used = block_scan(1, want, pref);
+    int most = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) most = max(most, sm_top[w]);
+    whole = used <= (int)gridDim.x && most <= q0 + q0 / 8 + 2 * kWarps;
+    if (whole) {
+      if (c >= used) return;
+      if (pref <= c && c < pref + want) {
+        sm_unit[0] = tid;
+        sm_unit[1] = pref;
+        sm_unit[2] = want;
+      }
     }
-    sm_item = s;
-    sm_base = base;
+  }
+  // the line: CTA cc takes tiles [bnd(cc), bnd(cc + 1))
+  const int P = min((int)gridDim.x, (N + kMinTiles - 1) / kMinTiles);
+  const int q = N / P, rem = N - q * P;
+  auto bnd = [&](int cc) { return cc * q + min(cc, rem); };
+  auto owner = [&](int t) { return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q; };
+  int r0 = 0, r1 = 1;
+  if (!whole) {
+    if (c >= P) return;
+    r0 = bnd(c);
+    r1 = bnd(c + 1);
+    if (mine > 0 && before <= r0 && r0 < before + mine) {  // one thread: tile r0 is among its own
+      int base = before, s = few ? tid / p.Hkv : tid * per;
+      if (few) {
+        base -= (tid % p.Hkv) * mine;                      // the item's first unit
+      } else {
+        for (;; ++s) {
+          const int t = tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
+          if (r0 < base + t) break;
+          base += t;
+        }
+      }
+      sm_unit[0] = s;
+      sm_unit[1] = base;
+    }
   }
   __syncthreads();
-  int s = sm_item;
-  long long base = sm_base;
+  int s = whole ? sm_unit[0] / p.Hkv : sm_unit[0], base = sm_unit[1];
   Item it = item_of(p, s, ROWS);
 
   while (r0 < r1) {
-    // ---- the next unit (it, g): tiles [ts, te) of the line, this CTA's up to r1 --------------
+    // ---- the next unit (it, g): its tiles [t_beg, t_end); CTAs c0 .. c0 + n - 1 share it -------
     int nt_item = tiles_of(it.npos);
-    while (r0 >= base + (long long)nt_item * p.Hkv) {
-      base += (long long)nt_item * p.Hkv;
-      it = item_of(p, ++s, ROWS);
-      nt_item = tiles_of(it.npos);
-    }
-    const int g = (int)((r0 - base) / nt_item);
-    const long long ts = base + (long long)g * nt_item, te = ts + nt_item;
-    const int t_beg = (int)(r0 - ts), t_end = (int)(min(r1, te) - ts);
-    const int b = it.b, row0 = it.rg * ROWS;
-
-    // ---- Q^T fragments: row gid of each row tile, the d order of the K fragments -----------
-    uint32_t qb[NQ][NT][KS][2];
-    float qs[NT][2];                             // score factor of rows 2 tig, 2 tig + 1
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int row = row0 + nt * 8 + gid;
-      const bool in = row < p.R;
-      const TQ* q = static_cast<const TQ*>(p.Q) + (in ? out_at(b, g, row) : 0);
-      if constexpr (FP8) {
-        float x[KS][4];
-        float mx = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const int d0 = 64 * (ks >> 2) + 16 * tig + 4 * (ks & 3);
-          if (!in) {
-            x[ks][0] = x[ks][1] = x[ks][2] = x[ks][3] = 0.f;
-          } else if constexpr (F32) {
-            const float4 v = *reinterpret_cast<const float4*>(q + d0);
-            x[ks][0] = v.x, x[ks][1] = v.y, x[ks][2] = v.z, x[ks][3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(q + d0);
-            unpack_bf16x2(v.x, x[ks][0], x[ks][1]);
-            unpack_bf16x2(v.y, x[ks][2], x[ks][3]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[ks][e]));
-        }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the row's largest element to [2^13, 2^14): e its exponent (zero or not finite: no shift)
-        const int e = (mx > 0.f && mx < INFINITY) ? ilogbf(mx) - 13 : 0;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float lo = ldexpf(x[ks][2 * i], -e), hi = ldexpf(x[ks][2 * i + 1], -e);
-            qb[0][nt][ks][i] = pack_f16x2(lo, hi);
-            if constexpr (F32) qb[1][nt][ks][i] = rest_f16x2(qb[0][nt][ks][i], lo, hi);
-          }
-        }
-        const float f = ldexpf(p.scale_log2, e);
-        qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
-        qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
-      } else if constexpr (CACHE == kFp32) {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const float4 v = in ? *reinterpret_cast<const float4*>(q + 16 * ks + 4 * tig) : make_float4(0.f, 0.f, 0.f, 0.f);
-          split3(v.x, v.y, qb[0][nt][ks][0], qb[1][nt][ks][0], qb[2][nt][ks][0]);
-          split3(v.z, v.w, qb[0][nt][ks][1], qb[1][nt][ks][1], qb[2][nt][ks][1]);
-        }
-        qs[nt][0] = qs[nt][1] = p.scale_log2;
-      } else {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          const uint2 v = in ? *reinterpret_cast<const uint2*>(q + 32 * (ks >> 1) + 8 * tig + 4 * (ks & 1)) : make_uint2(0u, 0u);
-          qb[0][nt][ks][0] = v.x;
-          qb[0][nt][ks][1] = v.y;
-        }
-        qs[nt][0] = qs[nt][1] = p.scale_log2;
+    int g, t_beg, t_end, c0, n;
+    if (whole) {
+      g = sm_unit[0] - s * p.Hkv;
+      c0 = sm_unit[1];
+      n = sm_unit[2];
+      const int qq = nt_item / n, rr = nt_item - qq * n, i = c - c0;
+      t_beg = i * qq + min(i, rr);
+      t_end = t_beg + qq + (i < rr ? 1 : 0);
+      r0 = r1;
+    } else {
+      while (r0 >= base + nt_item * p.Hkv) {
+        base += nt_item * p.Hkv;
+        it = item_of(p, ++s, ROWS);
+        nt_item = tiles_of(it.npos);
       }
+      g = (r0 - base) / nt_item;
+      const int ts = base + g * nt_item, te = ts + nt_item;
+      t_beg = r0 - ts;
+      t_end = min(r1, te) - ts;
+      c0 = owner(ts);
+      n = owner(te - 1) - c0 + 1;
+      r0 = min(r1, te);
     }
+    const int b = it.b, row0 = it.rg * ROWS, nr = min(ROWS, p.R - row0);
+    if (tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
 
     float o[NT][KS][4], l[NT][2], m[NT][2], mv[NT][2];
 #pragma unroll
@@ -390,6 +394,73 @@ __device__ void kernel_body(const Params& p) {
       for (int x = 0; x < (D * ES + 127) / 128; ++x) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 128 * x));
     };
 
+    // ---- Q^T fragments: row gid of each row tile, the d order of the K fragments -----------
+    uint32_t qb[NQ][NT][KS][2];
+    float qs[NT][2];                             // score factor of rows 2 tig, 2 tig + 1
+    auto load_q = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int row = row0 + nt * 8 + gid;
+        const bool in = row < p.R;
+        const TQ* q = static_cast<const TQ*>(p.Q) + (in ? out_at(b, g, row) : 0);
+        if constexpr (FP8) {
+          float x[KS][4];
+          float mx = 0.f;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const int d0 = 64 * (ks >> 2) + 16 * tig + 4 * (ks & 3);
+            if (!in) {
+              x[ks][0] = x[ks][1] = x[ks][2] = x[ks][3] = 0.f;
+            } else if constexpr (F32) {
+              const float4 v = *reinterpret_cast<const float4*>(q + d0);
+              x[ks][0] = v.x, x[ks][1] = v.y, x[ks][2] = v.z, x[ks][3] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(q + d0);
+              unpack_bf16x2(v.x, x[ks][0], x[ks][1]);
+              unpack_bf16x2(v.y, x[ks][2], x[ks][3]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx = fmaxf(mx, fabsf(x[ks][e]));
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // the row's largest element to [2^13, 2^14): e its exponent (zero or not finite: no shift)
+          const int e = (mx > 0.f && mx < INFINITY) ? (int)(__float_as_uint(mx) >> 23) - 127 - 13 : 0;
+          const int h1 = (-e) >> 1, h2 = -e - h1;    // in two steps: 2^-e may lie outside the floats
+          const float s1 = exp2_int(h1), s2 = exp2_int(h2);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float lo = x[ks][2 * i] * s1 * s2, hi = x[ks][2 * i + 1] * s1 * s2;
+              qb[0][nt][ks][i] = pack_f16x2(lo, hi);
+              if constexpr (F32) qb[1][nt][ks][i] = rest_f16x2(qb[0][nt][ks][i], lo, hi);
+            }
+          }
+          const float f = p.scale_log2 * exp2_int(-h1) * exp2_int(-h2);
+          qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
+          qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
+        } else if constexpr (CACHE == kFp32) {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const float4 v = in ? *reinterpret_cast<const float4*>(q + 16 * ks + 4 * tig) : make_float4(0.f, 0.f, 0.f, 0.f);
+            split3(v.x, v.y, qb[0][nt][ks][0], qb[1][nt][ks][0], qb[2][nt][ks][0]);
+            split3(v.z, v.w, qb[0][nt][ks][1], qb[1][nt][ks][1], qb[2][nt][ks][1]);
+          }
+          qs[nt][0] = qs[nt][1] = p.scale_log2;
+        } else {
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint2 v = in ? *reinterpret_cast<const uint2*>(q + 32 * (ks >> 1) + 8 * tig + 4 * (ks & 1)) : make_uint2(0u, 0u);
+            qb[0][nt][ks][0] = v.x;
+            qb[0][nt][ks][1] = v.y;
+          }
+          qs[nt][0] = qs[nt][1] = p.scale_log2;
+        }
+      }
+    };
+
+    if constexpr (!FP8) load_q();                // before the loads: there the registers are scarce
     int t = t_beg + warp;
 #pragma unroll
     for (int x = 1; x < kAhead; ++x) ahead(t + x * kWarps);
@@ -397,6 +468,8 @@ __device__ void kernel_body(const Params& p) {
     float sc = load_scale(tok);
     load_k(tok);
     load_v(tok);
+
+    if constexpr (FP8) load_q();
     for (; t < t_end; t += kWarps) {
       const int tok_nn = token(t + 2 * kWarps);
       ahead(t + kAhead * kWarps);
@@ -618,7 +691,6 @@ __device__ void kernel_body(const Params& p) {
       }
     }
     __syncthreads();
-    const int nr = min(ROWS, p.R - row0);
     auto row_stats = [&](int row, float& M, float& Mv, float& L) {
       M = Mv = kNone;
 #pragma unroll
@@ -643,10 +715,9 @@ __device__ void kernel_body(const Params& p) {
       return x;
     };
     auto lse_of = [&](int row, float M, float L) {
-      if (p.lse) p.lse[out_at(b, g, row0 + row) / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+      if (p.lse) p.lse[sm_off[row] / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     };
-    const int c0 = (int)(((ts + 1) * P - 1) / N), c1 = (int)((te * P - 1) / N);  // CTAs that share the unit
-    if (c0 == c1) {
+    if (n == 1) {
       for (int i = tid; i < nr * (D / 4); i += kThreads) {
         const int row = i / (D / 4);
         float M, Mv, L;
@@ -654,79 +725,80 @@ __device__ void kernel_body(const Params& p) {
         const float f = L == 0.f ? 0.f : (FP8 ? exp2f(Mv - M) : 1.f) / L;
         float4 x = warps_sum(i);
         x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-        store4(b, g, row0 + row, (i % (D / 4)) * 4, x);
+        store4(sm_off[row] + (i % (D / 4)) * 4, x);
         if (i % (D / 4) == 0) lse_of(row, M, L);
       }
       __syncthreads();  // shared memory is free again
-    } else {
-      // slot 0 of a CTA: the unit began before it; slot 1: the unit began here and goes on behind it
-      const auto slot = [&](int cc) { return p.part + (size_t)(2 * cc + (cc == c0 ? 1 : 0)) * slot_floats<D, NT>(); };
-      float* my = slot(c);
-      for (int i = tid; i < ROWS * (D / 4); i += kThreads) __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i));
-      if (tid < ROWS) {
-        float M, Mv, L;
-        row_stats(tid, M, Mv, L);
-        __stcg(my + ROWS * D + tid, M);
-        __stcg(my + ROWS * (D + 1) + tid, Mv);
-        __stcg(my + ROWS * (D + 2) + tid, L);
-      }
-      __threadfence();
-      __syncthreads();
-      uint32_t* ctr = p.counter + (size_t)s * p.Hkv + g;
-      if (tid == 0) sm_last = atomicAdd(ctr, 1u) == (uint32_t)(c1 - c0);
-      __syncthreads();
-      if (sm_last) {
-        __threadfence();
-        const int n = c1 - c0 + 1;
-        for (int row = warp; row < ROWS; row += kWarps) {
-          float M = kNone, Mv = kNone, L = 0.f;
-          for (int i = lane; i < n; i += 32) {
-            const float* q = slot(c0 + i) + ROWS * D + row;
-            M = fmaxf(M, __ldcg(q));
-            Mv = fmaxf(Mv, __ldcg(q + ROWS));
-          }
-          M = warp_max(M);
-          Mv = warp_max(Mv);
-          for (int i = lane; i < n; i += 32) {
-            const float* q = slot(c0 + i) + ROWS * D + row;
-            L += __ldcg(q + 2 * ROWS) * fast_exp2(__ldcg(q) - M);
-            sm_o[i * ROWS + row] = fast_exp2(__ldcg(q + ROWS) - Mv);
-          }
-          L = warp_sum(L);
-          if (lane == 0) {
-            sm_f[row] = L == 0.f ? 0.f : (FP8 ? exp2f(Mv - M) : 1.f) / L;
-            if (row < nr) lse_of(row, M, L);
-          }
+      continue;
+    }
+    // slot 1 of a CTA: the unit that begins in its stretch and goes on behind it (at most one);
+    // slot 0: the unit that began before it
+    const auto slot = [&](int i) { return p.part + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * slot_floats<D, NT>(); };
+    float* my = slot(c - c0);
+    for (int i = tid; i < ROWS * (D / 4); i += kThreads) __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i));
+    if (tid < ROWS) {
+      float M, Mv, L;
+      row_stats(tid, M, Mv, L);
+      __stcg(my + ROWS * D + tid, M);
+      __stcg(my + ROWS * (D + 1) + tid, Mv);
+      __stcg(my + ROWS * (D + 2) + tid, L);
+    }
+    uint32_t* ctr = p.counter + (size_t)s * p.Hkv + g;
+    __syncthreads();  // every thread's part is stored before the arrival, which releases them
+    if (tid == 0) sm_last = atom_add_acq_rel_gpu(ctr, 1u) == (uint32_t)(n - 1);
+    __syncthreads();
+    if (sm_last) {      // the others' parts, released before their arrivals
+      constexpr int kB = 16;  // loads in flight
+      float4 y[kB];
+      auto fetch = [&](int i, int j0) {
+#pragma unroll
+        for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(min(j0 + j, n - 1))) + i);
+      };
+      if (tid < nr * (D / 4)) fetch(tid, 0);
+      for (int row = warp; row < nr; row += kWarps) {
+        float M = kNone, Mv = kNone, L = 0.f;
+        for (int i = lane; i < n; i += 32) {
+          const float* x = slot(i) + ROWS * D + row;
+          const float mi = __ldcg(x), vi = __ldcg(x + ROWS), li = __ldcg(x + 2 * ROWS);
+          const float top = fmaxf(M, mi);
+          L = L * fast_exp2(M - top) + li * fast_exp2(mi - top);
+          M = top;
+          Mv = fmaxf(Mv, vi);
+          sm_o[i * ROWS + row] = vi;
         }
-        __syncthreads();
-        for (int i = tid; i < nr * (D / 4); i += kThreads) {
-          const int row = i / (D / 4);
-          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kB = 16;  // loads in flight
-          for (int j0 = 0; j0 < n; j0 += kB) {
-            float4 y[kB];
+        const float top = warp_max(M);
+        L = warp_sum(L * fast_exp2(M - top));
+        Mv = warp_max(Mv);
+        for (int i = lane; i < n; i += 32) sm_o[i * ROWS + row] = fast_exp2(sm_o[i * ROWS + row] - Mv);
+        if (lane == 0) {
+          sm_f[row] = L == 0.f ? 0.f : (FP8 ? exp2f(Mv - top) : 1.f) / L;
+          lse_of(row, top, L);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < nr * (D / 4); i += kThreads) {
+        const int row = i / (D / 4);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int j0 = 0; j0 < n; j0 += kB) {
+          if (i != tid || j0 > 0) fetch(i, j0);
 #pragma unroll
-            for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(c0 + min(j0 + j, n - 1))) + i);
-#pragma unroll
-            for (int j = 0; j < kB; ++j) {
-              const float w = j0 + j < n ? sm_o[(j0 + j) * ROWS + row] : 0.f;
-              if (j0 + j < n) {
-                x.x = fmaf(w, y[j].x, x.x);
-                x.y = fmaf(w, y[j].y, x.y);
-                x.z = fmaf(w, y[j].z, x.z);
-                x.w = fmaf(w, y[j].w, x.w);
-              }
+          for (int j = 0; j < kB; ++j) {
+            if (j0 + j < n) {
+              const float w = sm_o[(j0 + j) * ROWS + row];
+              x.x = fmaf(w, y[j].x, x.x);
+              x.y = fmaf(w, y[j].y, x.y);
+              x.z = fmaf(w, y[j].z, x.z);
+              x.w = fmaf(w, y[j].w, x.w);
             }
           }
-          const float f = sm_f[row];
-          x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-          store4(b, g, row0 + row, (i % (D / 4)) * 4, x);
         }
-        if (tid == 0) *ctr = 0u;  // clean for the next call
+        const float f = sm_f[row];
+        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+        store4(sm_off[row] + (i % (D / 4)) * 4, x);
       }
-      __syncthreads();
+      if (tid == 0) *ctr = 0u;  // clean for the next call
     }
-    r0 = min(r1, te);
+    __syncthreads();
   }
 }
 
