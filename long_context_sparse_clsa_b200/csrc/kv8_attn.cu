@@ -35,39 +35,31 @@ stream::Params params_of(const clsa_kv8_attn_args* a, float scale) {
   return p;
 }
 
-// calls f<F32, D, NT>
-template <typename F>
+// calls f<Cfg>: whole tiles of consecutive tokens come through the ring, an index list's by plain loads
+template <bool RING, typename F>
 auto dispatch(const clsa_kv8_attn_args* a, int R, F&& f) {
+  using namespace stream;
   const bool d128 = a->cache.d == 128;
   if (a->dtype == CLSA_F32)
-    return d128 ? f.template operator()<true, 128, 1>() : f.template operator()<true, 64, 1>();
-  if (stream::row_tiles(R, false) == 1)
-    return d128 ? f.template operator()<false, 128, 1>() : f.template operator()<false, 64, 1>();
-  return d128 ? f.template operator()<false, 128, 2>() : f.template operator()<false, 64, 2>();
+    return d128 ? f(Cfg<kE4m3, true, RING, 128, 1>{}) : f(Cfg<kE4m3, true, RING, 64, 1>{});
+  if (row_tiles(R, false) == 1)
+    return d128 ? f(Cfg<kE4m3, false, RING, 128, 1>{}) : f(Cfg<kE4m3, false, RING, 64, 1>{});
+  return d128 ? f(Cfg<kE4m3, false, RING, 128, 2>{}) : f(Cfg<kE4m3, false, RING, 64, 2>{});
 }
-
-struct Bytes {
-  const stream::Params& p;
-  template <bool F32, int D, int NT> size_t operator()() const { return stream::ws_bytes<stream::kE4m3, F32, D, NT>(p); }
-};
-struct Launch {
-  const stream::Params& p;
-  void* ws;
-  cudaStream_t s;
-  template <bool F32, int D, int NT> cudaError_t operator()() const { return stream::launch<stream::kE4m3, F32, D, NT>(p, ws, s); }
-};
 
 }  // namespace
 
 size_t kv8_attn_ws_bytes(const clsa_kv8_attn_args* a) {
   const stream::Params p = params_of(a, 1.f);
-  return dispatch(a, p.R, Bytes{p});
+  const auto f = [&](auto c) { return stream::ws_bytes<decltype(c)>(p); };
+  return a->idx ? dispatch<false>(a, p.R, f) : dispatch<true>(a, p.R, f);
 }
 
 cudaError_t launch_kv8_attn(const clsa_kv8_attn_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s) {
   stream::Params p = params_of(a, scale);
   p.ws_header = ws_header;
-  return dispatch(a, p.R, Launch{p, ws_body, s});
+  const auto f = [&](auto c) { return stream::launch<decltype(c)>(p, ws_body, s); };
+  return a->idx ? dispatch<false>(a, p.R, f) : dispatch<true>(a, p.R, f);
 }
 
 }  // namespace clsa

@@ -4,8 +4,7 @@
 //
 // What bounds it is moving K and V: with G query heads per KV head a byte of the cache feeds 2 G
 // multiplies.  So every warp is a stream of its own, with no barrier in its loop: it takes
-// tiles of 16 tokens, loads K and V straight into the registers that feed the tensor core
-// (mma.sync m16n8k16; a 128-row tcgen05 tile would be empty for G = 4), keeps a running
+// tiles of 16 tokens, brings K and V to the registers that feed the tensor core (mma.sync m16n8k16; a 128-row tcgen05 tile would be empty for G = 4), keeps a running
 // maximum, sum and output for its rows, and issues the next tile's loads as soon as the
 // registers are free.  Nothing of the cache passes through shared memory.
 //
@@ -37,10 +36,14 @@
 // order (the result does not depend on who that is).
 #pragma once
 
+#include <cuda.h>
+
 #include <algorithm>
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "kernels.h"
+#include "tma.h"
 
 namespace clsa {
 namespace stream {
@@ -72,11 +75,15 @@ struct Params {
   int T, window, sinks;     // T > 0: row r is the token count - T + r / G and sees a window and the sinks
   float scale_log2;
 };
+struct Maps {
+  CUtensorMap k, v;         // [seqs * n_max][Hkv * D] bytes, boxes of 16 tokens (ring only)
+};
 
 // a (sequence, row group): which tokens its rows see between them
 struct Item {
-  int b, rg, npos;          // npos positions; position i is token i (i < keep) or i + shift
-  int keep, shift, p0;      // p0: position of row 0 (window form)
+  int b, rg, npos;          // npos positions; position i < keepP is token i (none from keep on), the others i + shift
+  int keep, keepP, shift;   // keepP: keep rounded up to a tile, so that a tile's tokens are consecutive
+  int p0;                   // position of row 0 (window form)
 };
 
 __device__ __forceinline__ Item item_of(const Params& p, int s, int rows) {
@@ -87,8 +94,7 @@ __device__ __forceinline__ Item item_of(const Params& p, int s, int rows) {
   it.p0 = 0;
   if (p.T == 0) {
     it.npos = max(0, min(cnt, p.idx ? p.k : p.n_max));
-    it.keep = it.npos;
-    it.shift = 0;
+    it.keep = it.keepP = it.shift = 0;
     return it;
   }
   const int len = max(0, min(cnt, p.n_max));
@@ -96,14 +102,18 @@ __device__ __forceinline__ Item item_of(const Params& p, int s, int rows) {
   it.p0 = len - p.T;
   const int first = it.p0 + r0 / p.G, last = it.p0 + r1 / p.G;
   if (last < 0) {
-    it.npos = it.keep = it.shift = 0;
+    it.npos = it.keep = it.keepP = it.shift = 0;
     return it;
   }
   const int lo = max(0, first - p.window + 1);
   it.keep = min(p.sinks, lo);
-  it.shift = lo - it.keep;
-  it.npos = it.keep + last + 1 - lo;
+  it.keepP = (it.keep + kTile - 1) / kTile * kTile;
+  it.shift = lo - it.keepP;
+  it.npos = it.keepP + last + 1 - lo;
   return it;
+}
+__device__ __forceinline__ int token_of(const Item& it, int i) {  // token of position i, or -1
+  return i >= it.npos ? -1 : i >= it.keepP ? i + it.shift : i < it.keep ? i : -1;
 }
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -141,28 +151,45 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
 __device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
 __device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
 
+__device__ __forceinline__ int warp_scan_int(int v, int lane) {  // sum over the lanes up to this one
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int w = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += w;
+  }
+  return v;
+}
+__device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
 template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
 
-// warps of a CTA (one CTA per SM): what the registers allow, 168 or 255 a thread.  One large CTA
-// rather than three small: a unit that all SMs share has a third of the partials to merge.
-template <int CACHE, int NT>
-__host__ __device__ constexpr int warps_of() { return NT == 1 && CACHE != kFp32 ? 12 : 8; }
+// A variant: the kind of cache, fp32 rows, tiles through the ring, head dimension, row tiles.
+template <int CACHE_, bool F32_, bool RING_, int D_, int NT_>
+struct Cfg {
+  static constexpr int CACHE = CACHE_, D = D_, NT = NT_;
+  static constexpr bool F32 = F32_, RING = RING_;
+  static constexpr int ROWS = NT * 8;
+  static constexpr int ES = CACHE == kE4m3 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
+  static constexpr int RB = D * ES;                                       // bytes of a token's row
+  static constexpr int STAGE = 2 * kTile * RB;                            // K and V of a tile
+  // warps of a CTA (one CTA per SM): what the registers allow.  One large CTA rather than
+  // three small: a unit that all SMs share has a third of the partials to merge.
+  static constexpr int W = RING ? (NT == 2 ? 8 : 12) : (NT == 1 && CACHE != kFp32 ? 12 : 8);
+  static constexpr int NST = RING ? (192 * 1024 / (W * STAGE) < 6 ? 192 * 1024 / (W * STAGE) : 6) : 1;  // ring tiles of a warp
+  // dynamic shared memory: the ring; over it the warps' outputs, or the weights of P contributors
+  static size_t smem(int P) {
+    return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 4}) + 1024;
+  }
+};
 
-// shared memory: the warps' outputs, or the weights of up to P contributors
-template <int CACHE, int D, int NT>
-__host__ __device__ constexpr size_t smem_bytes(int P) {
-  const size_t o = (size_t)warps_of<CACHE, NT>() * NT * 8 * D * 4, w = (size_t)P * NT * 8 * 4;
-  return o > w ? o : w;
-}
-
-template <int CACHE, bool F32, int D, int NT>
-__device__ void kernel_body(const Params& p) {
+template <typename C>
+__device__ void kernel_body(const Maps& maps, const Params& p) {
+  constexpr int CACHE = C::CACHE, D = C::D, NT = C::NT, ROWS = C::ROWS, ES = C::ES, RB = C::RB, NST = C::NST;
+  constexpr bool F32 = C::F32, RING = C::RING, FP8 = CACHE == kE4m3;
   static_assert(F32 ? CACHE != kBf16 : CACHE != kFp32, "bf16 cache: bf16 rows; fp32 cache: fp32 rows");
-  constexpr bool FP8 = CACHE == kE4m3;
-  constexpr int kWarps = warps_of<CACHE, NT>(), kThreads = kWarps * 32;
-  constexpr int ROWS = NT * 8;
-  constexpr int ES = FP8 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
+  static_assert(!RING || NST >= 2, "a ring of two tiles at least");
+  constexpr int kWarps = C::W, kThreads = kWarps * 32;
   constexpr int KC = D * ES / 64;              // 16-byte chunks of a token's row that a lane takes
   constexpr int KS = D / 16;                   // k steps of S, d tiles of O
   constexpr int NQ = CACHE == kFp32 ? 3 : F32 ? 2 : 1;  // parts of a Q or P value
@@ -171,63 +198,44 @@ __device__ void kernel_body(const Params& p) {
   constexpr int VC = VB <= 16 ? 1 : VB / 16;
   using TQ = typename std::conditional<F32, float, __nv_bfloat16>::type;
 
-  extern __shared__ __align__(16) float sm_o[];
+  extern __shared__ __align__(1024) unsigned char sm_raw[];
+  unsigned char* const sm_base = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
+  float* const sm_o = reinterpret_cast<float*>(sm_base);
+  __shared__ uint64_t sm_full[RING ? kWarps : 1][RING ? NST : 1];
   __shared__ float sm_m[3][kWarps][ROWS];
+  __shared__ float sm_w[kWarps][ROWS];         // the warps' weights
   __shared__ float sm_f[ROWS];
   __shared__ long long sm_off[ROWS];           // where the unit's rows lie in Q and O
-  __shared__ int sm_scan[2][kWarps];
-  __shared__ int sm_top[kWarps];
-  __shared__ int sm_unit[4];
+  __shared__ int sm_scan[kWarps];
+  __shared__ int sm_unit[2];
   __shared__ int sm_last;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int nS = p.B * p.nrg, c = blockIdx.x;
+  if (RING && lane == 0) {                     // the warp's own barriers
+#pragma unroll
+    for (int i = 0; i < NST; ++i) mbar_init(&sm_full[warp][i], 1);
+    fence_mbar_init();
+  }
+  unsigned char* const ring = sm_base + (size_t)warp * NST * C::STAGE;
+  int issued = 0, used = 0;                    // tiles of the ring
+  bool dead = false;                           // a wait ran out
 
   // ---- the units' tiles, and how the CTAs share them ------------------------------------------
   auto tiles_of = [&](int npos) { return (npos + kTile - 1) / kTile; };
-  // sum of x over the threads, and over those before this one (two in turn: sm_scan has two rows)
-  auto block_scan = [&](int row, int x, int& before) {
-    int v = x;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int w = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += w;
-    }
-    if (lane == 31) sm_scan[row][warp] = v;
-    __syncthreads();
-    int sum = 0;
-    before = v - x;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += sm_scan[row][w];
-      sum += sm_scan[row][w];
-    }
-    return sum;
-  };
-  const int nU = nS * p.Hkv;
-  const bool few = nU <= (int)gridDim.x && nU <= kThreads;  // a thread per unit; else a run of items per thread
-  const int per = (nS + kThreads - 1) / kThreads;
-  int mine = 0, before;
-  if (few) {
-    if (tid < nU) mine = tiles_of(item_of(p, tid / p.Hkv, ROWS).npos);
-  } else {
-    for (int s = tid * per; s < min(nS, (tid + 1) * per); ++s) mine += tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
-  }
-  const int N = block_scan(0, mine, before);
-
   auto out_at = [&](int b, int g, int row) { return (long long)(row / p.G) * p.q_sl + b * p.q_sb + (long long)(g * p.G + row % p.G) * D; };
   auto store4 = [&](long long at, float4 x) {
     TQ* o = static_cast<TQ*>(p.O) + at;
     if constexpr (F32) *reinterpret_cast<float4*>(o) = x;
     else *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
   };
-
   // rows that see nothing: O = 0, lse = -inf
   for (int s = c; s < nS; s += gridDim.x) {
     const Item it = item_of(p, s, ROWS);
     if (it.npos > 0) continue;
     const int nr = min(ROWS, p.R - it.rg * ROWS);
+#pragma unroll 1
     for (int i = tid; i < p.Hkv * nr * (D / 4); i += kThreads) {
       const int g = i / (nr * (D / 4)), j = i % (nr * (D / 4));
       const long long at = out_at(it.b, g, it.rg * ROWS + j / (D / 4));
@@ -235,83 +243,113 @@ __device__ void kernel_body(const Params& p) {
       if (p.lse && j % (D / 4) == 0) p.lse[at / D] = -INFINITY;
     }
   }
-  if (N == 0) return;
 
-  // Two ways to share.  Whole CTAs per unit (a unit of x tiles takes x / q of them, q = tiles a CTA):
-  // no CTA works on two units one behind the other, and where a unit has one CTA there is
-  // nothing to merge.  Taken where it leaves no CTA more than an eighth (and two rounds of
-  // its warps) above q; else the line of all tiles is cut into equal stretches.
-  const int q0 = (N + (int)gridDim.x - 1) / (int)gridDim.x;
-  bool whole = few;
-  if (few) {
-    const int want = mine > 0 ? max(1, min(mine / q0, (mine + kMinTiles - 1) / kMinTiles)) : 0;
-    const int load = want > 0 ? (mine + want - 1) / want : 0;
-    const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)load);
-    if (lane == 0) sm_top[warp] = top;
-    int pref;
-    const int used = block_scan(1, want, pref);
-    int most = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) most = max(most, sm_top[w]);
-    whole = used <= (int)gridDim.x && most <= q0 + q0 / 8 + 2 * kWarps;
-    if (whole) {
-      if (c >= used) return;
-      if (pref <= c && c < pref + want) {
-        sm_unit[0] = tid;
-        sm_unit[1] = pref;
-        sm_unit[2] = want;
-      }
-    }
-  }
-  // the line: CTA cc takes tiles [bnd(cc), bnd(cc + 1))
-  const int P = min((int)gridDim.x, (N + kMinTiles - 1) / kMinTiles);
-  const int q = N / P, rem = N - q * P;
+  // Heads together: CTAs c, c + 1, ... take the heads of the same tokens, so that the cache's rows, which
+  // hold all heads, are read whole at about the same time.  Only where few CTAs stay idle for it.
+  const bool folded = p.Hkv <= (int)gridDim.x && (gridDim.x % p.Hkv) * 16 <= gridDim.x;
+  const int HG = folded ? p.Hkv : 1, nh = p.Hkv / HG;  // heads side by side, heads in the line
+  const int PG = gridDim.x / HG, cg = c / HG, gsub = c - cg * HG;
+  const int nU = nS * nh;
+  if (cg >= PG) return;
+  // Two ways to share.  Whole CTAs per unit (a unit of x of all N tiles takes x PG / N of them): no CTA
+  // works on two units one behind the other, and where a unit has one CTA there is nothing to
+  // merge.  Taken for few units, where it leaves no CTA more than an eighth (and two rounds of
+  // its warps) above N / PG; else the line of all units' tiles is cut into equal stretches.
+  bool whole = false;
+  int s, base = 0, r0 = 0, r1 = 1;               // item; its first tile in the line; this CTA's stretch
+  int u_g = 0, u_c0 = 0, u_n = 0;                // whole: the unit's head in the line, first CTA, CTAs
+  int N, P, q, rem;                              // CTA cc takes tiles [bnd(cc), bnd(cc + 1)) of N
   auto bnd = [&](int cc) { return cc * q + min(cc, rem); };
   auto owner = [&](int t) { return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q; };
-  int r0 = 0, r1 = 1;
-  if (!whole) {
-    if (c >= P) return;
-    r0 = bnd(c);
-    r1 = bnd(c + 1);
-    if (mine > 0 && before <= r0 && r0 < before + mine) {  // one thread: tile r0 is among its own
-      int base = before, s = few ? tid / p.Hkv : tid * per;
-      if (few) {
-        base -= (tid % p.Hkv) * mine;                      // the item's first unit
-      } else {
-        for (;; ++s) {
-          const int t = tiles_of(item_of(p, s, ROWS).npos) * p.Hkv;
-          if (r0 < base + t) break;
-          base += t;
-        }
-      }
-      sm_unit[0] = s;
-      sm_unit[1] = base;
+  if (nU <= 32) {                                // every warp for itself, a lane per unit
+    const int mine = lane < nU ? tiles_of(item_of(p, lane / nh, ROWS).npos) : 0;
+    N = warp_sum_int(mine);
+    if (N == 0) return;
+    const int fair = mine < (1 << 24) ? (int)((unsigned)mine * (unsigned)PG / (unsigned)N) : mine / ((N + PG - 1) / PG);
+    const int want = mine > 0 ? max(1, min(fair, (mine + kMinTiles - 1) / kMinTiles)) : 0;
+    const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(want > 0 ? (mine + want - 1) / want : 0));
+    const int pref = warp_scan_int(want, lane) - want, used = __shfl_sync(0xffffffffu, pref + want, 31);
+    whole = used <= PG && most <= N / PG + N / PG / 8 + 2 * kWarps;
+    if (whole) {
+      const unsigned here = __ballot_sync(0xffffffffu, pref <= cg && cg < pref + want);
+      if (here == 0) return;                     // more CTAs than wanted
+      const int u = __ffs(here) - 1;
+      s = u / nh;
+      u_g = u - s * nh;
+      u_c0 = __shfl_sync(0xffffffffu, pref, u);
+      u_n = __shfl_sync(0xffffffffu, want, u);
+    } else {
+      P = min(PG, (N + kMinTiles - 1) / kMinTiles);
+      q = N / P;
+      rem = N - q * P;
+      if (cg >= P) return;
+      r0 = bnd(cg);
+      r1 = bnd(cg + 1);
+      const int before = warp_scan_int(mine, lane) - mine;
+      const int u = __ffs(__ballot_sync(0xffffffffu, before <= r0 && r0 < before + mine)) - 1;
+      s = u / nh;
+      base = __shfl_sync(0xffffffffu, before, s * nh);
     }
+  } else {                                       // a run of items per thread
+    const int per = (nS + kThreads - 1) / kThreads;
+    int mine = 0;
+#pragma unroll 1
+    for (int x = tid * per; x < min(nS, (tid + 1) * per); ++x) mine += tiles_of(item_of(p, x, ROWS).npos) * nh;
+    const int scan = warp_scan_int(mine, lane);
+    if (lane == 31) sm_scan[warp] = scan;
+    __syncthreads();
+    N = 0;
+    int before = scan - mine;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sm_scan[w];
+      N += sm_scan[w];
+    }
+    if (N == 0) return;
+    P = min(PG, (N + kMinTiles - 1) / kMinTiles);
+    q = N / P;
+    rem = N - q * P;
+    if (cg >= P) return;
+    r0 = bnd(cg);
+    r1 = bnd(cg + 1);
+    if (mine > 0 && before <= r0 && r0 < before + mine) {  // one thread: tile r0 is among its own
+      int x = tid * per;
+#pragma unroll 1
+      for (;; ++x) {
+        const int t = tiles_of(item_of(p, x, ROWS).npos) * nh;
+        if (r0 < before + t) break;
+        before += t;
+      }
+      sm_unit[0] = x;
+      sm_unit[1] = before;
+    }
+    __syncthreads();
+    s = sm_unit[0];
+    base = sm_unit[1];
   }
-  __syncthreads();
-  int s = whole ? sm_unit[0] / p.Hkv : sm_unit[0], base = sm_unit[1];
   Item it = item_of(p, s, ROWS);
 
   while (r0 < r1) {
-    // ---- the next unit (it, g): its tiles [t_beg, t_end); CTAs c0 .. c0 + n - 1 share it -------
+    // ---- the next unit (it, g): its tiles [t_beg, t_end); CTA groups c0 .. c0 + n - 1 share it -------
     int nt_item = tiles_of(it.npos);
     int g, t_beg, t_end, c0, n;
     if (whole) {
-      g = sm_unit[0] - s * p.Hkv;
-      c0 = sm_unit[1];
-      n = sm_unit[2];
-      const int qq = nt_item / n, rr = nt_item - qq * n, i = c - c0;
+      g = folded ? gsub : u_g;
+      c0 = u_c0;
+      n = u_n;
+      const int qq = nt_item / n, rr = nt_item - qq * n, i = cg - c0;
       t_beg = i * qq + min(i, rr);
       t_end = t_beg + qq + (i < rr ? 1 : 0);
       r0 = r1;
     } else {
-      while (r0 >= base + nt_item * p.Hkv) {
-        base += nt_item * p.Hkv;
+      while (r0 >= base + nt_item * nh) {
+        base += nt_item * nh;
         it = item_of(p, ++s, ROWS);
         nt_item = tiles_of(it.npos);
       }
-      g = (r0 - base) / nt_item;
-      const int ts = base + g * nt_item, te = ts + nt_item;
+      const int x = (r0 - base) / nt_item;
+      g = folded ? gsub : x;
+      const int ts = base + x * nt_item, te = ts + nt_item;
       t_beg = r0 - ts;
       t_end = min(r1, te) - ts;
       c0 = owner(ts);
@@ -349,16 +387,38 @@ __device__ void kernel_body(const Params& p) {
     auto token = [&](int t) {
       const int i = t * kTile + (lane & 15);
       if (t >= t_end || i >= it.npos) return -1;
-      if (FP8 && p.idx) {
+      if (!RING && FP8) {
         const int tk = __ldg(p.idx + (size_t)b * p.k + i);
         if ((unsigned)tk < (unsigned)p.n_max) return tk;
         if (lane < 16) record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)i);
         return -1;
       }
-      return i < it.keep ? i : i + it.shift;
+      return FP8 ? i : token_of(it, i);
     };
-    uint4 kr[2][KC];
-    VecV vr[4][VC];
+    // the ring: tile t by TMA, 128 bytes of 16 tokens a box, swizzled by the TMA unit
+    auto issue = [&](int t) {
+      if (t >= t_end || dead) return;
+      if (lane == 0) {
+        const int slot = issued % NST;
+        uint64_t* bar = &sm_full[warp][slot];
+        unsigned char* dst = ring + slot * C::STAGE;
+        const int i = t * kTile, row = (int)seq * p.n_max + (FP8 || i < it.keepP ? i : i + it.shift);
+        mbar_arrive_expect_tx(bar, C::STAGE);
+#pragma unroll
+        for (int x = 0; x < (RB + 127) / 128; ++x) {
+          tma_load_2d(dst + 2048 * x, &maps.k, g * RB + 128 * x, row, bar);
+          tma_load_2d(dst + kTile * RB + 2048 * x, &maps.v, g * RB + 128 * x, row, bar);
+        }
+      }
+      ++issued;
+    };
+    // byte offset of 16-byte chunk ch of token r's row in a stage (ch counts through the row)
+    auto chunk = [&](int r, int ch) {
+      if constexpr (RB == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+      else return (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    };
+    uint4 kr[2][KC];                             // K: tokens gid, gid + 8
+    VecV vr[4][VC];                              // V: tokens 2 tig, 2 tig + 1, + 8, + 9
     auto load_k = [&](int tok) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -384,15 +444,6 @@ __device__ void kernel_body(const Params& p) {
       }
     };
     auto load_scale = [&](int tok) { return FP8 && tok >= 0 ? __ldg(scp + (size_t)(tok >> p.bshift) * p.Hkv) : 1.f; };
-
-    // the tokens' lines of tile t on their way into L2 (a lane per row; selections are small)
-    auto ahead = [&](int t) {
-      const int i = t * kTile + (lane & 15);
-      if ((FP8 && p.idx) || t >= t_end || i >= it.npos) return;
-      const uint8_t* a = (lane < 16 ? kb : vb) + (size_t)(i < it.keep ? i : i + it.shift) * rstr;
-#pragma unroll
-      for (int x = 0; x < (D * ES + 127) / 128; ++x) asm volatile("prefetch.global.L2 [%0];" ::"l"(a + 128 * x));
-    };
 
     // ---- Q^T fragments: row gid of each row tile, the d order of the K fragments -----------
     uint32_t qb[NQ][NT][KS][2];
@@ -424,20 +475,19 @@ __device__ void kernel_body(const Params& p) {
           }
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // the row's largest element to [2^13, 2^14): e its exponent (zero or not finite: no shift)
-          const int e = (mx > 0.f && mx < INFINITY) ? (int)(__float_as_uint(mx) >> 23) - 127 - 13 : 0;
-          const int h1 = (-e) >> 1, h2 = -e - h1;    // in two steps: 2^-e may lie outside the floats
-          const float s1 = exp2_int(h1), s2 = exp2_int(h2);
+          // the row's largest element to [2^13, 2^14): e its exponent (not finite: no shift)
+          const int e = mx < INFINITY ? max((int)(__float_as_uint(mx) >> 23) - 127 - 13, -126) : 0;
+          const float s1 = exp2_int(-e);
 #pragma unroll
           for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float lo = x[ks][2 * i] * s1 * s2, hi = x[ks][2 * i + 1] * s1 * s2;
+              const float lo = x[ks][2 * i] * s1, hi = x[ks][2 * i + 1] * s1;
               qb[0][nt][ks][i] = pack_f16x2(lo, hi);
               if constexpr (F32) qb[1][nt][ks][i] = rest_f16x2(qb[0][nt][ks][i], lo, hi);
             }
           }
-          const float f = p.scale_log2 * exp2_int(-h1) * exp2_int(-h2);
+          const float f = p.scale_log2 * exp2_int(e);
           qs[nt][0] = __shfl_sync(0xffffffffu, f, 8 * tig);
           qs[nt][1] = __shfl_sync(0xffffffffu, f, 8 * tig + 4);
         } else if constexpr (CACHE == kFp32) {
@@ -461,18 +511,41 @@ __device__ void kernel_body(const Params& p) {
     };
 
     if constexpr (!FP8) load_q();                // before the loads: there the registers are scarce
-    int t = t_beg + warp;
+    int t = t_beg + warp, tok = -1, tok_n = -1;
+    float sc;
+    if constexpr (RING) {
 #pragma unroll
-    for (int x = 1; x < kAhead; ++x) ahead(t + x * kWarps);
-    int tok = token(t), tok_n = token(t + kWarps);
-    float sc = load_scale(tok);
-    load_k(tok);
-    load_v(tok);
-
+      for (int x = 0; x < NST; ++x) issue(t + x * kWarps);
+      tok = token(t);
+      sc = load_scale(tok);
+    } else {
+      tok = token(t);
+      tok_n = token(t + kWarps);
+      sc = load_scale(tok);
+      load_k(tok);
+      load_v(tok);
+    }
     if constexpr (FP8) load_q();
     for (; t < t_end; t += kWarps) {
-      const int tok_nn = token(t + 2 * kWarps);
-      ahead(t + kAhead * kWarps);
+      int tok_nn = -1;
+      unsigned char* stage = nullptr;
+      if constexpr (RING) {
+        const int slot = used % NST;
+        if (!dead && !mbar_wait_warp(&sm_full[warp][slot], (uint32_t)(used / NST) & 1u)) {
+          if (lane == 0) record_error(p.ws_header, CLSA_ERR_TIMEOUT, 70);
+          dead = true;
+        }
+        ++used;
+        stage = ring + slot * C::STAGE;
+        tok_n = token(t + kWarps);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < KC; ++i)
+            kr[h][i] = *reinterpret_cast<const uint4*>(stage + chunk(gid + 8 * h, 4 * i + tig));
+      } else {
+        tok_nn = token(t + 2 * kWarps);
+      }
       // S^T
       float sa[NT][4];
 #pragma unroll
@@ -514,7 +587,29 @@ __device__ void kernel_body(const Params& p) {
           }
         }
       }
-      load_k(tok_n);
+      if constexpr (RING) {
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const int r = 2 * tig + (h & 1) + 8 * (h >> 1);
+#pragma unroll
+          for (int i = 0; i < VC; ++i) {
+            if constexpr (VB == 8) vr[h][i] = *reinterpret_cast<const uint2*>(stage + kTile * RB + chunk(r, gid >> 1) + 8 * (gid & 1));
+            else vr[h][i] = *reinterpret_cast<const uint4*>(stage + kTile * RB + chunk(r, 8 * i + gid));
+          }
+        }
+        // a tile with places that hold no token of the unit: whatever lies there, V = 0
+        if (!__all_sync(0xffffffffu, tok >= 0)) {
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int tk = __shfl_sync(0xffffffffu, tok, 2 * tig + (h & 1) + 8 * (h >> 1));
+#pragma unroll
+            for (int i = 0; i < VC; ++i)
+              if (tk < 0) vr[h][i] = VecV{};
+          }
+        }
+      } else {
+        load_k(tok_n);
+      }
       // scores of tokens gid, gid + 8 (h) and rows 2 tig, 2 tig + 1 (x): sa[nt][2 h + x]
       const int tk[2] = {__shfl_sync(0xffffffffu, tok, gid), __shfl_sync(0xffffffffu, tok, gid + 8)};
       float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
@@ -650,9 +745,20 @@ __device__ void kernel_body(const Params& p) {
           }
         }
       }
-      load_v(tok_n);
+      if constexpr (RING) {
+        __syncwarp();                            // the stage has been used: the next tile may overwrite it
+        issue(t + NST * kWarps);
+      } else {
+        load_v(tok_n);
+      }
       tok = tok_n;
       tok_n = tok_nn;
+    }
+    if constexpr (RING) {
+      if (dead) {                                // loads in flight land before their memory has another use
+        for (; used < issued; ++used) mbar_wait_warp(&sm_full[warp][used % NST], (uint32_t)(used / NST) & 1u);
+      }
+      __syncthreads();                           // the warps' outputs go over the ring
     }
 
     // ---- the warps' results to one -----------------------------------------------------------
@@ -669,17 +775,8 @@ __device__ void kernel_body(const Params& p) {
         }
       }
     }
-    __syncthreads();
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float f[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float top = kNone;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[1][w][nt * 8 + 2 * tig + x]);
-        f[x] = fast_exp2(mv[nt][x] - top);
-      }
 #pragma unroll
       for (int j = 0; j < KS; ++j) {
         const int d0 = FP8 ? gid * (D / 8) + 2 * j
@@ -687,30 +784,38 @@ __device__ void kernel_body(const Params& p) {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           *reinterpret_cast<float2*>(sm_o + ((size_t)warp * ROWS + nt * 8 + 2 * tig + x) * D + d0) =
-              make_float2(o[nt][j][x] * f[x], o[nt][j][2 + x] * f[x]);
+              make_float2(o[nt][j][x], o[nt][j][2 + x]);
       }
     }
     __syncthreads();
-    auto row_stats = [&](int row, float& M, float& Mv, float& L) {
-      M = Mv = kNone;
-#pragma unroll
+    // a thread per (warp, row): the warp's weight; the first of a row: the row's references and sum
+    float M = kNone, Mv = kNone, L = 0.f;
+    if (tid < kWarps * ROWS) {
+      const int w0 = tid / ROWS, row = tid % ROWS;
+#pragma unroll 4
       for (int w = 0; w < kWarps; ++w) {
         M = fmaxf(M, sm_m[0][w][row]);
         Mv = fmaxf(Mv, sm_m[1][w][row]);
       }
-      L = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) L += sm_m[2][w][row] * fast_exp2(sm_m[0][w][row] - M);
-    };
+      sm_w[w0][row] = fast_exp2(sm_m[1][w0][row] - Mv);
+      if (w0 == 0) {
+#pragma unroll 4
+        for (int w = 0; w < kWarps; ++w) L += sm_m[2][w][row] * fast_exp2(sm_m[0][w][row] - M);
+        sm_f[row] = L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L;
+      }
+    }
+    __syncthreads();
     auto warps_sum = [&](int i) {  // float4 i of the unit's rows, over the warps
+      const int row = i / (D / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 4
       for (int w = 0; w < kWarps; ++w) {
         const float4 y = *reinterpret_cast<const float4*>(sm_o + (size_t)w * ROWS * D + 4 * i);
-        x.x += y.x;
-        x.y += y.y;
-        x.z += y.z;
-        x.w += y.w;
+        const float f = sm_w[w][row];
+        x.x = fmaf(f, y.x, x.x);
+        x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z);
+        x.w = fmaf(f, y.w, x.w);
       }
       return x;
     };
@@ -720,25 +825,24 @@ __device__ void kernel_body(const Params& p) {
     if (n == 1) {
       for (int i = tid; i < nr * (D / 4); i += kThreads) {
         const int row = i / (D / 4);
-        float M, Mv, L;
-        row_stats(row, M, Mv, L);
-        const float f = L == 0.f ? 0.f : (FP8 ? exp2f(Mv - M) : 1.f) / L;
+        const float f = sm_f[row];
         float4 x = warps_sum(i);
         x.x *= f, x.y *= f, x.z *= f, x.w *= f;
         store4(sm_off[row] + (i % (D / 4)) * 4, x);
-        if (i % (D / 4) == 0) lse_of(row, M, L);
       }
-      __syncthreads();  // shared memory is free again
+      if (tid < nr) lse_of(tid, M, L);
+      if (RING) fence_proxy_async_smem();        // before the next unit's TMA writes
+      __syncthreads();                           // shared memory is free again
       continue;
     }
     // slot 1 of a CTA: the unit that begins in its stretch and goes on behind it (at most one);
     // slot 0: the unit that began before it
-    const auto slot = [&](int i) { return p.part + (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * slot_floats<D, NT>(); };
-    float* my = slot(c - c0);
+    float* const part0 = p.part + (size_t)(2 * (c0 * HG + gsub)) * slot_floats<D, NT>();
+    const int step = 2 * HG * slot_floats<D, NT>();
+    const auto slot = [&](int i) { return part0 + (i * step + (i == 0 ? slot_floats<D, NT>() : 0)); };
+    float* my = slot(cg - c0);
     for (int i = tid; i < ROWS * (D / 4); i += kThreads) __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i));
     if (tid < ROWS) {
-      float M, Mv, L;
-      row_stats(tid, M, Mv, L);
       __stcg(my + ROWS * D + tid, M);
       __stcg(my + ROWS * (D + 1) + tid, Mv);
       __stcg(my + ROWS * (D + 2) + tid, L);
@@ -748,7 +852,7 @@ __device__ void kernel_body(const Params& p) {
     if (tid == 0) sm_last = atom_add_acq_rel_gpu(ctr, 1u) == (uint32_t)(n - 1);
     __syncthreads();
     if (sm_last) {      // the others' parts, released before their arrivals
-      constexpr int kB = 16;  // loads in flight
+      constexpr int kB = 8;  // loads in flight
       float4 y[kB];
       auto fetch = [&](int i, int j0) {
 #pragma unroll
@@ -756,7 +860,8 @@ __device__ void kernel_body(const Params& p) {
       };
       if (tid < nr * (D / 4)) fetch(tid, 0);
       for (int row = warp; row < nr; row += kWarps) {
-        float M = kNone, Mv = kNone, L = 0.f;
+        M = Mv = kNone;
+        L = 0.f;
         for (int i = lane; i < n; i += 32) {
           const float* x = slot(i) + ROWS * D + row;
           const float mi = __ldcg(x), vi = __ldcg(x + ROWS), li = __ldcg(x + 2 * ROWS);
@@ -771,7 +876,7 @@ __device__ void kernel_body(const Params& p) {
         Mv = warp_max(Mv);
         for (int i = lane; i < n; i += 32) sm_o[i * ROWS + row] = fast_exp2(sm_o[i * ROWS + row] - Mv);
         if (lane == 0) {
-          sm_f[row] = L == 0.f ? 0.f : (FP8 ? exp2f(Mv - top) : 1.f) / L;
+          sm_f[row] = L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - top) : 1.f) / L;
           lse_of(row, top, L);
         }
       }
@@ -798,14 +903,15 @@ __device__ void kernel_body(const Params& p) {
       }
       if (tid == 0) *ctr = 0u;  // clean for the next call
     }
+    if (RING) fence_proxy_async_smem();
     __syncthreads();
   }
 }
 
-template <int CACHE, bool F32, int D, int NT>
-__global__ void __launch_bounds__(warps_of<CACHE, NT>() * 32, 1) stream_attn_kernel(const Params p) {
+template <typename C>
+__global__ void __launch_bounds__(C::W * 32, 1) stream_attn_kernel(const __grid_constant__ Maps maps, const Params p) {
   pdl_enter();
-  kernel_body<CACHE, F32, D, NT>(p);
+  kernel_body<C>(maps, p);
 }
 
 inline size_t counter_bytes(const Params& p) { return align_up((size_t)p.B * p.nrg * p.Hkv * 4, 256); }
@@ -813,21 +919,46 @@ inline size_t counter_bytes(const Params& p) { return align_up((size_t)p.B * p.n
 // the row groups of R rows: one or two row tiles
 inline int row_tiles(int R, bool f32) { return R <= 8 || f32 ? 1 : 2; }
 
-template <int CACHE, bool F32, int D, int NT>
-size_t ws_bytes(const Params& p) {
-  const int P = std::max(1, device_info().sm_count);
-  return counter_bytes(p) + (size_t)2 * P * slot_floats<D, NT>() * 4;
+// 2-D map of bytes [rows][row_bytes], boxes of 16 rows and up to 128 bytes
+inline bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes) {
+  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static EncodeFn fn = nullptr;
+  if (!fn) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult st;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &st) != cudaSuccess || !f) return false;
+    fn = reinterpret_cast<EncodeFn>(f);
+  }
+  const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_bytes, kTile}, es[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            box_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_64B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int CACHE, bool F32, int D, int NT>
+template <typename C>
+size_t ws_bytes(const Params& p) {
+  const int P = std::max(1, device_info().sm_count);
+  return counter_bytes(p) + (size_t)2 * P * slot_floats<C::D, C::NT>() * 4;
+}
+
+template <typename C>
 cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   const int P = std::max(1, device_info().sm_count);
   p.counter = static_cast<uint32_t*>(ws_body);
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
-  const size_t smem = smem_bytes<CACHE, D, NT>(P);
-  auto* k = stream_attn_kernel<CACHE, F32, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3(P), dim3(warps_of<CACHE, NT>() * 32), smem, s, p);
+  Maps maps{};
+  if (C::RING) {
+    const uint64_t rows = (uint64_t)p.seqs * p.n_max, bytes = (uint64_t)p.Hkv * C::RB;
+    if (!make_map(&maps.k, p.K, rows, bytes, std::min(C::RB, 128)) || !make_map(&maps.v, p.V, rows, bytes, std::min(C::RB, 128)))
+      return cudaErrorInvalidValue;
+  }
+  const size_t smem = C::smem(P);
+  cudaError_t e = cudaFuncSetAttribute(stream_attn_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = launch_pdl(stream_attn_kernel<C>, dim3(P), dim3(C::W * 32), smem, s, maps, p);
   launches_add(1, s);
   return e;
 }

@@ -30,27 +30,15 @@ stream::Params params_of(const clsa_window_args* a, float scale) {
   return p;
 }
 
-// calls f<CACHE, F32, D, NT>
+// calls f<Cfg>
 template <typename F>
 auto dispatch(const clsa_window_args* a, int R, F&& f) {
+  using namespace stream;
   const bool d128 = a->d == 128;
-  if (a->dtype == CLSA_F32)
-    return d128 ? f.template operator()<stream::kFp32, true, 128, 1>() : f.template operator()<stream::kFp32, true, 64, 1>();
-  if (stream::row_tiles(R, false) == 1)
-    return d128 ? f.template operator()<stream::kBf16, false, 128, 1>() : f.template operator()<stream::kBf16, false, 64, 1>();
-  return d128 ? f.template operator()<stream::kBf16, false, 128, 2>() : f.template operator()<stream::kBf16, false, 64, 2>();
+  if (a->dtype == CLSA_F32) return d128 ? f(Cfg<kFp32, true, false, 128, 1>{}) : f(Cfg<kFp32, true, false, 64, 1>{});
+  if (row_tiles(R, false) == 1) return d128 ? f(Cfg<kBf16, false, true, 128, 1>{}) : f(Cfg<kBf16, false, true, 64, 1>{});
+  return d128 ? f(Cfg<kBf16, false, true, 128, 2>{}) : f(Cfg<kBf16, false, true, 64, 2>{});
 }
-
-struct Bytes {
-  const stream::Params& p;
-  template <int C, bool F32, int D, int NT> size_t operator()() const { return stream::ws_bytes<C, F32, D, NT>(p); }
-};
-struct Launch {
-  const stream::Params& p;
-  void* ws;
-  cudaStream_t s;
-  template <int C, bool F32, int D, int NT> cudaError_t operator()() const { return stream::launch<C, F32, D, NT>(p, ws, s); }
-};
 
 // chunks with more rows per KV head than this run in row tiles of 128 on tcgen05
 constexpr long long kStreamRows = 64;
@@ -64,14 +52,14 @@ bool use_tc(const clsa_window_args* a) {
 size_t window_attn_ws_bytes(const clsa_window_args* a) {
   if (use_tc(a)) return 0;
   const stream::Params p = params_of(a, 1.f);
-  return dispatch(a, p.R, Bytes{p});
+  return dispatch(a, p.R, [&](auto c) { return stream::ws_bytes<decltype(c)>(p); });
 }
 
 cudaError_t launch_window_attn(const clsa_window_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s) {
   if (use_tc(a)) return launch_window_tc(a, scale, ws_header, s);
   stream::Params p = params_of(a, scale);
   p.ws_header = ws_header;
-  return dispatch(a, p.R, Launch{p, ws_body, s});
+  return dispatch(a, p.R, [&](auto c) { return stream::launch<decltype(c)>(p, ws_body, s); });
 }
 
 }  // namespace clsa
