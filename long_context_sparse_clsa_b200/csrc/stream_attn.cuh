@@ -49,7 +49,7 @@ namespace clsa {
 namespace stream {
 
 constexpr int kTile = 16;                   // tokens of a tile
-constexpr int kMinTiles = 4;                // fewest tiles worth a CTA
+constexpr int kMinTiles = 12;               // fewest tiles worth a CTA (one a warp)
 constexpr int kAhead = 4;                   // tiles of a warp between its L2 prefetch and its loads
 constexpr float kNone = -3e38f;             // reference of a row that has seen nothing
 constexpr float kTau = 8.f;
@@ -511,6 +511,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     };
 
     if constexpr (!FP8) load_q();                // before the loads: there the registers are scarce
+    const int nw = min(kWarps, t_end - t_beg);   // warps that have a tile
     int t = t_beg + warp, tok = -1, tok_n = -1;
     float sc;
     if constexpr (RING) {
@@ -525,7 +526,9 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       load_k(tok);
       load_v(tok);
     }
-    if constexpr (FP8) load_q();
+    if constexpr (FP8) {
+      if (warp < nw) load_q();
+    }
     for (; t < t_end; t += kWarps) {
       int tok_nn = -1;
       unsigned char* stage = nullptr;
@@ -762,45 +765,45 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     }
 
     // ---- the warps' results to one -----------------------------------------------------------
+    // float4 `ch` of a warp's row, placed so that neither its writers nor its readers collide
+    auto so = [&](int w, int row, int ch) { return reinterpret_cast<float4*>(sm_o) + (w * ROWS + row) * (D / 4) + (ch ^ ((row >> 1) & 3)); };
+    if (warp < nw) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
+        for (int x = 0; x < 2; ++x) {
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
-        if (gid == 0) {
-          sm_m[0][warp][nt * 8 + 2 * tig + x] = m[nt][x];
-          sm_m[1][warp][nt * 8 + 2 * tig + x] = mv[nt][x];
-          sm_m[2][warp][nt * 8 + 2 * tig + x] = l[nt][x];
+          for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+          if (gid == 0) {
+            sm_m[0][warp][nt * 8 + 2 * tig + x] = m[nt][x];
+            sm_m[1][warp][nt * 8 + 2 * tig + x] = mv[nt][x];
+            sm_m[2][warp][nt * 8 + 2 * tig + x] = l[nt][x];
+          }
         }
-      }
-    }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+        for (int j = 0; j < KS; j += 2) {          // two d tiles: 4 elements of d in a row
+          const int ch = FP8 ? gid * (D / 32) + j / 2
+                             : CACHE == kBf16 ? 16 * (j >> 2) + 2 * gid + ((j & 3) >> 1) : 8 * (j >> 1) + gid;
 #pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        const int d0 = FP8 ? gid * (D / 8) + 2 * j
-                           : CACHE == kBf16 ? 64 * (j >> 2) + 8 * gid + 2 * (j & 3) : 32 * (j >> 1) + 4 * gid + 2 * (j & 1);
-#pragma unroll
-        for (int x = 0; x < 2; ++x)
-          *reinterpret_cast<float2*>(sm_o + ((size_t)warp * ROWS + nt * 8 + 2 * tig + x) * D + d0) =
-              make_float2(o[nt][j][x], o[nt][j][2 + x]);
+          for (int x = 0; x < 2; ++x)
+            *so(warp, nt * 8 + 2 * tig + x, ch) = make_float4(o[nt][j][x], o[nt][j][2 + x], o[nt][j + 1][x], o[nt][j + 1][2 + x]);
+        }
       }
     }
     __syncthreads();
     // a thread per (warp, row): the warp's weight; the first of a row: the row's references and sum
     float M = kNone, Mv = kNone, L = 0.f;
-    if (tid < kWarps * ROWS) {
+    if (tid < nw * ROWS) {
       const int w0 = tid / ROWS, row = tid % ROWS;
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
+      for (int w = 0; w < nw; ++w) {
         M = fmaxf(M, sm_m[0][w][row]);
         Mv = fmaxf(Mv, sm_m[1][w][row]);
       }
       sm_w[w0][row] = fast_exp2(sm_m[1][w0][row] - Mv);
       if (w0 == 0) {
 #pragma unroll 4
-        for (int w = 0; w < kWarps; ++w) L += sm_m[2][w][row] * fast_exp2(sm_m[0][w][row] - M);
+        for (int w = 0; w < nw; ++w) L += sm_m[2][w][row] * fast_exp2(sm_m[0][w][row] - M);
         sm_f[row] = L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L;
       }
     }
@@ -809,8 +812,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       const int row = i / (D / 4);
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int w = 0; w < kWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(sm_o + (size_t)w * ROWS * D + 4 * i);
+      for (int w = 0; w < nw; ++w) {
+        const float4 y = *so(w, row, i % (D / 4));
         const float f = sm_w[w][row];
         x.x = fmaf(f, y.x, x.x);
         x.y = fmaf(f, y.y, x.y);

@@ -29,6 +29,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -114,6 +115,15 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
       "[%5];" ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
       : "memory");
 }
+// one lane of a converged warp.  MMAs are issued under it, and with operands that are the same in
+// every lane by construction: then a tcgen05.mma issues in the 64 cycles that it runs (M128 N128
+// K16); under `lane == 0` each took about 140.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -163,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   uint64_t* p_full = bars + 22;              // [2][2]: the halves of P
   uint64_t* o_full = bars + 26;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (warp == 0) {
     tc::tmem_alloc(tmem_slot, 512);
@@ -263,32 +273,51 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       return true;
     };
     auto full = [&](int idx, int site) { return wait(kv_full + idx % S::slots, (uint32_t)(idx / S::slots) & 1u, site); };
-    auto qk = [&](int t, int idx) {  // S_t = Q_t K^T
-      if (lane == 0) {
-        const uint32_t qa = smem_u32(base + t * S::tile), ka = smem_u32(base + S::ring + (idx % S::slots) * S::tile);
+    const uint64_t q0 = tc::sw128_desc(smem_u32(base)), ring0 = tc::sw128_desc(smem_u32(base + S::ring));
+    const uint64_t ringv0 = tc::sw128_desc_mn(smem_u32(base + S::ring), kAtom);
+    auto qk = [&](auto t, int slot) {  // S_t = Q_t K^T
+      const uint64_t qd = q0 + t * (S::tile >> 4), kd = ring0 + (uint32_t)slot * (S::tile >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          tc::mma_bf16(tmem + 128u * t, tc::sw128_desc(qa + (ks >> 2) * kAtom + (ks & 3) * 32),
-                       tc::sw128_desc(ka + (ks >> 2) * kAtom + (ks & 3) * 32), idesc_qk, ks > 0);
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint32_t off = ((ks >> 2) * kAtom + (ks & 3) * 32) >> 4;
+          tc::mma_bf16(tmem + 128u * t, qd + off, kd + off, idesc_qk, ks > 0);
+        }
         tc::mma_commit(s_full + t);
       }
+      __syncwarp();
+    };
+    auto pv = [&](auto t, int h, int slot, bool more_than_one) {  // O_t += P_t V, token rows [64 h, 64 h + 64)
+      const uint64_t vd = ringv0 + (uint32_t)slot * (S::tile >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * (4 * h + ks), vd + (uint32_t)(4 * h + ks) * (16 * 128 >> 4), idesc_pv,
+                      more_than_one || ks > 0);
+      }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) tc::mma_commit(bar);
       __syncwarp();
     };
     int i = blockIdx.x;
     WItem w;
     w.nkv = 0;
     while (i < p.items && (w = witem(p, i)).nkv == 0) i += gridDim.x;
+    auto first = [&](auto t) {
+      if (t >= w.ntile || !ok) return;
+      ok = wait(q_full + t, nq[t]++ & 1u, 63);
+      if (!ok) return;
+      tc::fence_after_sync();
+      qk(t, uniform(n % S::slots));
+      if (w.nkv == 1) commit(q_empty + t);
+    };
     if (i < p.items) {  // the first item's first scores
       ok = full(n, 62);
-      for (int t = 0; t < w.ntile && ok; ++t) {
-        ok = wait(q_full + t, nq[t]++ & 1u, 63);
-        if (ok) {
-          tc::fence_after_sync();
-          qk(t, n);
-          if (w.nkv == 1 && lane == 0) tc::mma_commit(q_empty + t);
-        }
-      }
-      if (ok && lane == 0) tc::mma_commit(kv_empty + n % S::slots);
+      first(std::integral_constant<int, 0>{});
+      first(std::integral_constant<int, 1>{});
+      if (ok) commit(kv_empty + n % S::slots);
     }
     int j = 0;
     while (i < p.items && ok) {
@@ -317,43 +346,35 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
         __syncwarp();
       }
       bool have_k = false;
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        if (t < w.ntile) {
-          const uint32_t va = smem_u32(base + S::ring + vslot * S::tile);
+      const int vs = uniform(vslot), ks = uniform((n + 2) % S::slots);
+      const bool later = uniform(j) > 0;
+      auto step = [&](auto t) {
+        if (t < w.ntile && ok) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             ok = ok && wait(p_full + 2 * t + h, np[t] & 1u, 65);
-            if (!ok) break;
+            if (!ok) return;
             tc::fence_after_sync();
-            if (lane == 0) {
-#pragma unroll
-              for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
-                mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, tc::sw128_desc_mn(va + ks * 16 * 128, kAtom), idesc_pv,
-                            j > 0 || ks > 0);
-              if (h == 1 && j == w.nkv - 1) tc::mma_commit(o_full + t);
-            }
+            pv(t, h, vs, later || h > 0);
           }
-          if (!ok) break;
           ++np[t];
-          __syncwarp();
+          if (j == w.nkv - 1) commit(o_full + t);
         }
-        if (more && t < nw.ntile) {
+        if (more && t < nw.ntile && ok) {
           if (!have_k) ok = full(n + 2, 66);
           have_k = true;
           if (ok && nj == 0) ok = wait(q_full + t, nq[t]++ & 1u, 67);
-          if (!ok) break;
+          if (!ok) return;
           tc::fence_after_sync();
-          qk(t, n + 2);
-          if (nj == nw.nkv - 1 && lane == 0) tc::mma_commit(q_empty + t);
+          qk(t, ks);
+          if (nj == nw.nkv - 1) commit(q_empty + t);
         }
-      }
+      };
+      step(std::integral_constant<int, 0>{});
+      step(std::integral_constant<int, 1>{});
       if (!ok) break;
-      if (lane == 0) {
-        tc::mma_commit(kv_empty + vslot);
-        if (more) tc::mma_commit(kv_empty + (n + 2) % S::slots);
-      }
-      __syncwarp();
+      commit(kv_empty + vs);
+      if (more) commit(kv_empty + ks);
       n += 2;
       w = nw;
       i = ni;
