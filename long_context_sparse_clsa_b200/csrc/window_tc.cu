@@ -12,8 +12,8 @@
 // sees are zeroed in shared memory, so their bytes do not matter (0 * NaN).
 //
 // Roles (one CTA per SM, persistent over items): one warp issues TMA loads into a ring of K and V
-// tiles; one warp issues the MMAs; two groups of four warps each own one row tile's softmax,
-// a thread a row.  For every token tile and row tile i:
+// tiles; one zeroes the unseen value rows; one issues the MMAs; two groups of four warps each own
+// one row tile's softmax, a thread a row.  For every token tile and row tile i:
 //   S_i = Q_i K^T        M128 N128, both operands in shared memory      -> TMEM
 //   P_i = exp2(S_i scale - m)   S from TMEM to registers, bf16 P back over S's columns
 //   O_i += P_i V         A = P from TMEM, B = V (MN-major)              -> TMEM
@@ -42,8 +42,9 @@ namespace {
 
 constexpr int kTok = 128;                   // tokens of a tile
 constexpr int kRows = 128;                  // rows of a row tile
-constexpr int kSoftWarps = 8;
-constexpr int kThreadsW = (kSoftWarps + 2) * 32;  // + loads, MMAs
+// Warp roles.  The MMA warp comes first: it is the one that must never wait for an issue slot.
+constexpr int kMmaWarp = 0, kTmaWarp = 1, kFixWarp = 2, kSoft0 = 4;  // kSoft0 + 0..3: row tile 0, + 4..7: row tile 1
+constexpr int kThreadsW = (kSoft0 + 8) * 32;
 constexpr uint32_t kAtom = 128 * 128;       // 128 rows x 128 bytes
 constexpr float kNone = -3e38f;
 constexpr float kTau = 8.f;
@@ -67,9 +68,10 @@ struct Smem {
   static constexpr int KA = D / 64;                     // 64-column atoms
   static constexpr uint32_t tile = KA * kAtom;          // Q, K or V tile
   static constexpr int slots = D == 128 ? 5 : 8;        // K and V tiles in the ring
+  static_assert(slots <= 8, "at most four V tiles");
   static constexpr uint32_t ring = 2 * tile;            // after the two Q tiles
   static constexpr uint32_t bars = ring + slots * tile;
-  static constexpr uint32_t total = bars + 256 + 1024;  // + alignment of the base
+  static constexpr uint32_t total = bars + 272 + 1024;  // + alignment of the base
 };
 
 // an item: rows [t0, t1) of sequence b, KV head g, and its line of tokens
@@ -123,6 +125,19 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
   return p != 0;
 }
+// bounded wait of a whole warp; false (and CLSA_ERR_TIMEOUT with `site`) once kWaitLimitNs has passed
+__device__ __forceinline__ bool wait_full(uint64_t* bar, uint32_t parity, void* ws, int site) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const unsigned long long t0 = globaltimer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int x = 0; x < 32; ++x)
+      if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > kWaitLimitNs)) break;
+  }
+  if ((threadIdx.x & 31) == 0) record_error(ws, CLSA_ERR_TIMEOUT, site);
+  return false;
+}
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 // D[tmem] (+)= A[tmem] * B[smem]
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -172,7 +187,10 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   uint64_t* s_full = bars + 20;
   uint64_t* p_full = bars + 22;              // [2][2]: the halves of P
   uint64_t* o_full = bars + 26;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 28);
+  // a V tile's unseen rows are zero; such tiles take the four in turn (the ring holds at most four V
+  // tiles, so the warp that zeroes them is never a whole turn ahead)
+  uint64_t* fixed = bars + 28;               // [4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
 
   if (warp == 0) {
@@ -192,6 +210,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       mbar_init(p_full + 2 * i + 1, 4);
       mbar_init(o_full + i, 1);
     }
+    for (int i = 0; i < 4; ++i) mbar_init(fixed + i, 1);
     fence_mbar_init();
   }
   tc::fence_before_sync();
@@ -199,7 +218,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;  // S_i at 128 i (P_i over its first 64 columns), O_i at 256 + 128 i
 
-  if (warp == kSoftWarps) {
+  if (warp == kTmaWarp) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
       int n = 0;              // K and V tiles issued
@@ -258,25 +277,44 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       for (int t = 0; t < 2; ++t)
         if (qi[t] > 0) mbar_wait(q_full + t, (qi[t] - 1) & 1u);
     }
-  } else if (warp == kSoftWarps + 1) {
+  } else if (warp == kFixWarp) {
+    // ---------------------------------------------------------------- value rows that no row sees
+    int n = 0, nfix = 0;       // ring position, tiles zeroed
+    bool ok = true;
+    for (int i = blockIdx.x; i < p.items && ok; i += gridDim.x) {
+      const WItem w = witem(p, i);
+      for (int j = 0; j < w.nkv && ok; ++j, n += 2) {
+        // every phase in its turn (a wait for a phase that lies two ahead would pass at once)
+        for (int x = n; x < n + 2 && ok; ++x)
+          ok = wait_full(kv_full + x % S::slots, (uint32_t)(x / S::slots) & 1u, p.ws_header, 72);
+        int a0, a1, b0;
+        if (!ok || !dead_rows(w, j, a0, a1, b0)) continue;
+        unsigned char* v = base + S::ring + ((n + 1) % S::slots) * S::tile;
+        for (int x = lane; x < (a1 - a0 + kTok - b0) * 8; x += 32) {
+          const int r = x >> 3, row = r < a1 - a0 ? a0 + r : b0 + r - (a1 - a0);
+#pragma unroll
+          for (int a = 0; a < S::KA; ++a)
+            *reinterpret_cast<uint4*>(v + a * kAtom + row * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(fixed + (nfix & 3));
+        ++nfix;
+      }
+    }
+  } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMAs
     constexpr uint32_t idesc_qk = tc::idesc_bf16_f32(kRows, kTok);
     constexpr uint32_t idesc_pv = tc::idesc_bf16_f32(kRows, D) | (1u << 16);  // V MN-major
-    int n = 0;                 // ring position of the current step's K tile
-    uint32_t nq[2] = {0, 0}, np[2] = {0, 0};
-    bool ok = true;
-    auto wait = [&](uint64_t* bar, uint32_t parity, int site) {
-      if (!mbar_wait_warp(bar, parity)) {
-        if (lane == 0) record_error(p.ws_header, CLSA_ERR_TIMEOUT, site);
-        return false;
-      }
-      return true;
-    };
-    auto full = [&](int idx, int site) { return wait(kv_full + idx % S::slots, (uint32_t)(idx / S::slots) & 1u, site); };
     const uint64_t q0 = tc::sw128_desc(smem_u32(base)), ring0 = tc::sw128_desc(smem_u32(base + S::ring));
     const uint64_t ringv0 = tc::sw128_desc_mn(smem_u32(base + S::ring), kAtom);
-    auto qk = [&](auto t, int slot) {  // S_t = Q_t K^T
-      const uint64_t qd = q0 + t * (S::tile >> 4), kd = ring0 + (uint32_t)slot * (S::tile >> 4);
+    int slot = 0;              // ring position of the current step's K tile, and how often the ring was gone through
+    uint32_t use = 0, nq[2] = {0, 0}, np = 0, np1 = 0, nfix = 0;  // phases
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity, int site) { return wait_full(bar, parity & 1u, p.ws_header, site); };
+    auto qk = [&](auto t, int at) {  // S_t = Q_t K^T
+      const uint64_t qd = q0 + t * (S::tile >> 4), kd = ring0 + (uint32_t)uniform(at) * (S::tile >> 4);
+      tc::fence_after_sync();
       if (elect_one()) {
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
@@ -287,13 +325,13 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       }
       __syncwarp();
     };
-    auto pv = [&](auto t, int h, int slot, bool more_than_one) {  // O_t += P_t V, token rows [64 h, 64 h + 64)
-      const uint64_t vd = ringv0 + (uint32_t)slot * (S::tile >> 4);
+    auto pv = [&](auto t, auto h, int at, bool add) {  // O_t += P_t V, tokens [64 h, 64 h + 64)
+      const uint64_t vd = ringv0 + (uint32_t)uniform(at) * (S::tile >> 4);
+      tc::fence_after_sync();
       if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * (4 * h + ks), vd + (uint32_t)(4 * h + ks) * (16 * 128 >> 4), idesc_pv,
-                      more_than_one || ks > 0);
+        for (int ks = 4 * h; ks < 4 * h + 4; ++ks)
+          mma_bf16_ts(tmem + 256u + 128u * t, tmem + 128u * t + 8u * ks, vd + (uint32_t)ks * (16 * 128 >> 4), idesc_pv, add || ks > 0);
       }
       __syncwarp();
     };
@@ -301,25 +339,23 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       if (elect_one()) tc::mma_commit(bar);
       __syncwarp();
     };
-    int i = blockIdx.x;
+    int i = blockIdx.x, j = 0;
     WItem w;
     w.nkv = 0;
     while (i < p.items && (w = witem(p, i)).nkv == 0) i += gridDim.x;
-    auto first = [&](auto t) {
-      if (t >= w.ntile || !ok) return;
-      ok = wait(q_full + t, nq[t]++ & 1u, 63);
-      if (!ok) return;
-      tc::fence_after_sync();
-      qk(t, uniform(n % S::slots));
-      if (w.nkv == 1) commit(q_empty + t);
-    };
-    if (i < p.items) {  // the first item's first scores
-      ok = full(n, 62);
+    if (i < p.items) {         // the first item's first scores
+      ok = wait(kv_full, 0, 62);
+      auto first = [&](auto t) {
+        if (t >= w.ntile || !ok) return;
+        ok = wait(q_full + t, nq[t]++, 63);
+        if (!ok) return;
+        qk(t, 0);
+        if (w.nkv == 1) commit(q_empty + t);
+      };
       first(std::integral_constant<int, 0>{});
       first(std::integral_constant<int, 1>{});
-      if (ok) commit(kv_empty + n % S::slots);
+      if (ok) commit(kv_empty);
     }
-    int j = 0;
     while (i < p.items && ok) {
       // the step behind this one: the item's next token tile, or the next item's first
       WItem nw = w;
@@ -330,59 +366,51 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
         while (ni < p.items && (nw = witem(p, ni)).nkv == 0);
       }
       const bool more = ni < p.items;
-      const int vslot = (n + 1) % S::slots;
-      ok = full(n + 1, 64);
-      if (!ok) break;
+      int vslot = slot + 1, kslot = slot + 2;
+      uint32_t vuse = use, kuse = use;
+      if (vslot >= S::slots) vslot -= S::slots, ++vuse;
+      if (kslot >= S::slots) kslot -= S::slots, ++kuse;
       int a0, a1, b0;
-      if (dead_rows(w, j, a0, a1, b0)) {  // value rows that no row sees
-        unsigned char* v = base + S::ring + vslot * S::tile;
-        for (int x = lane; x < (a1 - a0 + kTok - b0) * 8; x += 32) {
-          const int r = x >> 3, row = r < a1 - a0 ? a0 + r : b0 + r - (a1 - a0);
-#pragma unroll
-          for (int a = 0; a < S::KA; ++a)
-            *reinterpret_cast<uint4*>(v + a * kAtom + row * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
+      const bool fix = dead_rows(w, j, a0, a1, b0);
+      ok = fix ? wait(fixed + (nfix & 3), nfix >> 2, 71) : wait(kv_full + vslot, vuse, 64);
+      nfix += fix ? 1 : 0;
       bool have_k = false;
-      const int vs = uniform(vslot), ks = uniform((n + 2) % S::slots);
-      const bool later = uniform(j) > 0;
       auto step = [&](auto t) {
         if (t < w.ntile && ok) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            ok = ok && wait(p_full + 2 * t + h, np[t] & 1u, 65);
-            if (!ok) return;
-            tc::fence_after_sync();
-            pv(t, h, vs, later || h > 0);
-          }
-          ++np[t];
+          const uint32_t ph = t == 0 ? np : np1;
+          ok = wait(p_full + 2 * t, ph, 65);
+          if (!ok) return;
+          pv(t, std::integral_constant<int, 0>{}, vslot, j > 0);
+          ok = wait(p_full + 2 * t + 1, ph, 65);
+          if (!ok) return;
+          pv(t, std::integral_constant<int, 1>{}, vslot, true);
+          if (t == 0) ++np;
+          else ++np1;
           if (j == w.nkv - 1) commit(o_full + t);
         }
         if (more && t < nw.ntile && ok) {
-          if (!have_k) ok = full(n + 2, 66);
+          if (!have_k) ok = wait(kv_full + kslot, kuse, 66);
           have_k = true;
-          if (ok && nj == 0) ok = wait(q_full + t, nq[t]++ & 1u, 67);
+          if (ok && nj == 0) ok = wait(q_full + t, nq[t]++, 67);
           if (!ok) return;
-          tc::fence_after_sync();
-          qk(t, ks);
+          qk(t, kslot);
           if (nj == nw.nkv - 1) commit(q_empty + t);
         }
       };
       step(std::integral_constant<int, 0>{});
       step(std::integral_constant<int, 1>{});
       if (!ok) break;
-      commit(kv_empty + vs);
-      if (more) commit(kv_empty + ks);
-      n += 2;
+      commit(kv_empty + vslot);
+      if (more) commit(kv_empty + kslot);
+      slot = kslot;
+      use = kuse;
       w = nw;
       i = ni;
       j = nj;
     }
-  } else if (warp < kSoftWarps) {
+  } else if (warp >= kSoft0) {
     // ---------------------------------------------------------------- softmax
-    const int t = warp >> 2;                        // row tile
+    const int t = (warp - kSoft0) >> 2;                        // row tile
     const int r = (warp & 3) * 32 + lane;           // row of the tile
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + 128u * t, to = tmem + lanes + 256u + 128u * t;
@@ -399,11 +427,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       const int pf = w.len - p.T + w.t0 + t * p.TQ, pl = pf + p.TQ - 1;
       float m = kNone, l = 0.f;
       for (int j = 0; j < w.nkv; ++j) {
-        if (!mbar_wait(s_full + t, ns++ & 1u)) {
-          record_error(p.ws_header, CLSA_ERR_TIMEOUT, 68);
-          ok = false;
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        ok = wait_full(s_full + t, ns++ & 1u, p.ws_header, 68);
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t v[kTok];
@@ -479,11 +503,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       if (!ok) break;
       uint4* out = reinterpret_cast<uint4*>(p.O + row * D);
       if (w.nkv > 0) {
-        if (!mbar_wait(o_full + t, no++ & 1u)) {
-          record_error(p.ws_header, CLSA_ERR_TIMEOUT, 69);
-          ok = false;
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        ok = wait_full(o_full + t, no++ & 1u, p.ws_header, 69);
         if (!ok) break;
         tc::fence_after_sync();
         const float inv = l == 0.f ? 0.f : 1.f / l;
