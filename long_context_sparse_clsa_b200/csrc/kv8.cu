@@ -75,6 +75,7 @@ struct WriteParams {
 // One CTA per (sequence, block of tokens that the new rows touch, head, K or V): the block's
 // new rows stay in registers between their maximum and their codes, so they are read once.
 // A thread holds NU units of 16 elements.  No two CTAs share a block's scale or codes.
+// 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64: 36.9 us.
 template <typename T, int NU>
 __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams p) {
   pdl_enter();
@@ -99,8 +100,8 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
   const int first = blk * p.block;         // the block's first token
   const int lo = max(first, p0);           // new rows of this block: tokens [lo, hi)
   const int hi = min(first + p.block, p0 + cnt);
-  const int upr = p.d / 16;                // units per row
-  const int units = (hi - lo) * upr;
+  const int sh = p.d == 128 ? 3 : 2, mask = (1 << sh) - 1;  // a row has 8 or 4 units
+  const int units = (hi - lo) << sh;
   const T* src = static_cast<const T*>(isv ? p.V : p.K) + (((size_t)b * p.T + (lo - p0)) * p.Hkv + h) * p.d;
   const size_t rstr = (size_t)p.Hkv * p.d;
   uint8_t* codes = (isv ? p.V8 : p.K8) + ((size_t)b * p.n_max * p.Hkv + h) * p.d;
@@ -113,7 +114,7 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int v = threadIdx.x + i * kThreadsW;
-    if (v < units) x[i].load(src + (size_t)(v / upr) * rstr + (v % upr) * 16);
+    if (v < units) x[i].load(src + (size_t)(v >> sh) * rstr + (v & mask) * 16);
     else x[i].zero();
   }
 #pragma unroll
@@ -142,15 +143,15 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
         const float2 f = x[i].pair(2 * e), g = x[i].pair(2 * e + 1);
         w[e] = (uint32_t)f32x2_to_e4m3x2(f.x * inv, f.y * inv) | ((uint32_t)f32x2_to_e4m3x2(g.x * inv, g.y * inv) << 16);
       }
-      *reinterpret_cast<uint4*>(codes + (size_t)(lo + v / upr) * rstr + (v % upr) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   if (threadIdx.x == 0 && !(kept && s == s_old)) *sc = s;
   if (kept && s > s_old) {                 // the earlier rows move to the larger scale
     const float r = s_old * inv;
-    const int old_units = (lo - first) * upr;
+    const int old_units = (lo - first) << sh;
     for (int v = threadIdx.x; v < old_units; v += kThreadsW) {
-      uint4* at = reinterpret_cast<uint4*>(codes + (size_t)(first + v / upr) * rstr + (v % upr) * 16);
+      uint4* at = reinterpret_cast<uint4*>(codes + (size_t)(first + (v >> sh)) * rstr + (v & mask) * 16);
       uint4 q = *at;
       uint32_t* w = reinterpret_cast<uint32_t*>(&q);
 #pragma unroll
@@ -177,53 +178,50 @@ struct ReadParams {
   int B, T, n_max, Hkv, d, bshift, nblk, tpc;
 };
 
-// A CTA takes tpc rows of one sequence; its units of 16 codes run over (row, K or V, head,
-// part of d), so neighbouring threads read and write neighbouring bytes.
+// A thread keeps its place in the row (threadIdx.x: 16 codes of a head, threadIdx.y: the head,
+// blockIdx.y: K or V and the heads behind blockDim.y) and walks the rows of the CTA, kReadRows of
+// them in flight: no divisions in the loop.  4 x 8001 rows of 8 x 128 as bf16: 34.1 us with two rows,
+// 38 with four, 44 with eight (more registers, fewer threads); 42 with a flat index.
+constexpr int kReadRows = 2;
 template <typename T>
-__global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p) {
+__global__ void __launch_bounds__(256, 5) kv8_read_kernel(const ReadParams p) {
   pdl_enter();
   const int ctas = (p.T + p.tpc - 1) / p.tpc;  // per sequence
   const int b = blockIdx.x / ctas;
   const int t0 = (blockIdx.x - b * ctas) * p.tpc;
   const int cnt = p.count ? min(p.count[b], p.T) : p.T;
-  const int nrow = min(p.tpc, cnt - t0);
-  if (nrow <= 0) return;
-  const int upr = p.Hkv * p.d / 16;            // units of one row of K (or V)
-  const int uph = p.d / 16;
+  const int t1 = min(t0 + p.tpc, cnt);
+  const bool isv = blockIdx.y & 1u;
+  const int h = (blockIdx.y >> 1) * blockDim.y + threadIdx.y;
+  if (t0 >= t1 || h >= p.Hkv) return;
+  const size_t rstr = (size_t)p.Hkv * p.d;
+  const int col = h * p.d + threadIdx.x * 16;
+  const uint8_t* codes = (isv ? p.V8 : p.K8) + (size_t)b * p.n_max * rstr + col;
+  const float* scales = (isv ? p.vs : p.ks) + (size_t)b * p.nblk * p.Hkv + h;
+  T* out = static_cast<T*>(isv ? p.V : p.K) + (size_t)b * p.T * rstr + col;
   const long long s0 = p.start ? p.start[b] : 0;
-  for (int u0 = threadIdx.x; u0 < nrow * 2 * upr; u0 += 4 * blockDim.x) {
-    uint4 c[4];
-    float s[4];
-    size_t dst[4];
-    bool ok[4], isv[4];
+  for (int t = t0 + threadIdx.z; t < t1; t += kReadRows * blockDim.z) {
+    uint4 c[kReadRows];
+    float s[kReadRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int u = u0 + i * blockDim.x;
-      ok[i] = u < nrow * 2 * upr;
-      if (!ok[i]) continue;
-      const int r = u / (2 * upr);
-      int w = u - r * 2 * upr;
-      isv[i] = w >= upr;
-      if (isv[i]) w -= upr;
-      const int t = t0 + r;
-      const long long tok = p.idx ? p.idx[(size_t)b * p.T + t] : s0 + t;
-      const bool in = tok >= 0 && tok < p.n_max;
-      dst[i] = ((size_t)b * p.T + t) * p.Hkv * p.d + (size_t)w * 16;
+    for (int i = 0; i < kReadRows; ++i) {
+      const int ti = t + i * blockDim.z;
+      if (ti >= t1) continue;
+      const long long tok = p.idx ? p.idx[(size_t)b * p.T + ti] : s0 + ti;
       c[i] = make_uint4(0u, 0u, 0u, 0u);
       s[i] = 0.f;
-      if (in) {
-        const size_t row = (size_t)b * p.n_max + (size_t)tok;
-        c[i] = ld_stream_v4((isv[i] ? p.V8 : p.K8) + row * p.Hkv * p.d + (size_t)w * 16);
-        s[i] = __ldg((isv[i] ? p.vs : p.ks) + ((size_t)b * p.nblk + (size_t)(tok >> p.bshift)) * p.Hkv + w / uph);
-      } else if (w == 0 && !isv[i]) {
-        record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)t);
+      if (tok >= 0 && tok < p.n_max) {
+        c[i] = ld_stream_v4(codes + (size_t)tok * rstr);
+        s[i] = __ldg(scales + (size_t)(tok >> p.bshift) * p.Hkv);
+      } else if (col == 0 && !isv) {
+        record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)ti);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (!ok[i]) continue;
+    for (int i = 0; i < kReadRows; ++i) {
+      const int ti = t + i * blockDim.z;
+      if (ti >= t1) continue;
       const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-      T* out = static_cast<T*>(isv[i] ? p.V : p.K) + dst[i];
       float f[16];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -232,13 +230,13 @@ __global__ void __launch_bounds__(256) kv8_read_kernel(const ReadParams p) {
         f[2 * e + 1] = x.y * s[i];
       }
       if constexpr (sizeof(T) == 2) {
-        uint4* o = reinterpret_cast<uint4*>(out);
+        uint4* o = reinterpret_cast<uint4*>(out + (size_t)ti * rstr);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
           o[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
                             pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
       } else {
-        float4* o = reinterpret_cast<float4*>(out);
+        float4* o = reinterpret_cast<float4*>(out + (size_t)ti * rstr);
 #pragma unroll
         for (int q = 0; q < 4; ++q) o[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
       }
@@ -295,12 +293,16 @@ cudaError_t launch_kv8_write(const clsa_kv8_cache* c, const void* K, const void*
   return e;
 }
 
-// rows a CTA takes: about 4 units a thread
-static int read_tpc(const clsa_kv8_cache* c) { return std::max(1, 1024 / (2 * c->Hkv * c->d / 16)); }
+// threads of a CTA: a head's units, heads, rows (256 in all); rows a CTA takes
+static dim3 read_block(const clsa_kv8_cache* c) {
+  const int x = c->d / 16, y = std::min(c->Hkv, 256 / x);
+  return dim3(x, y, std::max(1, 256 / (x * y)));
+}
+static int read_tpc(const clsa_kv8_cache* c) { return kReadRows * (int)read_block(c).z; }
 
 bool kv8_read_grid_ok(const clsa_kv8_cache* c, int T) {
   const int tpc = read_tpc(c);
-  return ((long long)T + tpc - 1) / tpc * c->B <= 0x7fffffffLL && 2LL * tpc * c->Hkv * c->d / 16 < (1LL << 30);
+  return ((long long)T + tpc - 1) / tpc * c->B <= 0x7fffffffLL && c->Hkv <= 1 << 16;
 }
 
 cudaError_t launch_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const int32_t* idx, const int32_t* count,
@@ -324,9 +326,10 @@ cudaError_t launch_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const
   p.bshift = log2_of(c->block);
   p.nblk = (c->n_max + c->block - 1) / c->block;
   p.tpc = read_tpc(c);
-  const dim3 grid((unsigned)(((long long)T + p.tpc - 1) / p.tpc * c->B));
-  const cudaError_t e = dt == CLSA_BF16 ? launch_pdl(kv8_read_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, p)
-                                        : launch_pdl(kv8_read_kernel<float>, grid, dim3(256), 0, s, p);
+  const dim3 block = read_block(c);
+  const dim3 grid((unsigned)(((long long)T + p.tpc - 1) / p.tpc * c->B), 2 * ((c->Hkv + block.y - 1) / block.y));
+  const cudaError_t e = dt == CLSA_BF16 ? launch_pdl(kv8_read_kernel<__nv_bfloat16>, grid, block, 0, s, p)
+                                        : launch_pdl(kv8_read_kernel<float>, grid, block, 0, s, p);
   launches_add(1, s);
   return e;
 }

@@ -26,6 +26,7 @@ namespace {
 constexpr int kMaxPairs = 64;      // d <= 128
 constexpr int kMaxTokRope = 16;    // tokens per CTA
 constexpr int kMaxThreadsRope = 256;
+constexpr int kHeads = 5;               // heads of a thread in flight
 
 struct RopeParams {
   const void* q;
@@ -36,7 +37,6 @@ struct RopeParams {
   int n_pos, jq, jk;   // rows n + j n_pos, j < jq (queries) and j < jk (keys), share position n
   int Hq, Hk, d, rot;
   int tpc;             // tokens per CTA
-  int uph, upt;        // units per head, per token
   float mscale, sign;  // sign: -1 for the transpose
   double turns[kMaxPairs];
 };
@@ -67,96 +67,92 @@ template <> struct Vec16<float> {
   }
 };
 
-// one unit: where it lies, what kind it is, and its data
-struct RopeUnit {
-  const uint4* src = nullptr;  // null: no unit
-  uint4* dst = nullptr;
-  int tok = 0, c = 0;          // token of the CTA; vector of the head (of the first half, for "half")
-  uint4 a, b;
-};
-
+// A thread owns one vector (c, threadIdx.x) of the heads of one token (threadIdx.z): its cosines and
+// sines stay in registers while it walks the heads threadIdx.y, + blockDim.y, ..., kHeads of
+// them in flight.  (With a flat index and a table look-up per vector the kernel was bound by its
+// own instructions: 127 us for 671 MB, against the figure above.)
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams p) {
   pdl_enter();
-  constexpr int N = Vec16<T>::N;
-  __shared__ float2 tab[kMaxTokRope][kMaxPairs];
-  const int n0 = blockIdx.x * p.tpc;
-  const int ntok = min(p.tpc, p.n_pos - n0);
+  constexpr int N = Vec16<T>::N, NC = HALF ? N : N / 2;  // elements, pairs of a vector
+  __shared__ __align__(16) float2 tab[kMaxTokRope][kMaxPairs];
   const int half = p.rot / 2;
-  const int total = ntok * p.upt;
-  const int nt = blockDim.x;
-  const int rv = HALF ? half / N : p.rot / N;   // units of a head that are turned
-
-  auto locate = [&](int u) {
-    RopeUnit r;
-    if (u >= total) return r;
-    r.tok = u / p.upt;
-    const int w = u - r.tok * p.upt;
-    int hh = w / p.uph;
-    r.c = w - hh * p.uph;
-    const bool isq = hh < p.jq * p.Hq;
-    if (!isq) hh -= p.jq * p.Hq;
-    const int H = isq ? p.Hq : p.Hk;
-    const int j = hh / H, h = hh - j * H;
-    const size_t row = (size_t)j * p.n_pos + n0 + r.tok;
-    // the vector of the head: a pass-through unit c >= rv lies rv further on in "half"
-    const int v = r.c < rv ? r.c : r.c + (HALF ? rv : 0);
-    const size_t off = (row * H + h) * p.d + (size_t)v * N;
-    r.src = reinterpret_cast<const uint4*>(static_cast<const T*>(isq ? p.q : p.k) + off);
-    r.dst = reinterpret_cast<uint4*>(static_cast<T*>(isq ? p.q_out : p.k_out) + off);
-    r.a = __ldcs(r.src);
-    if (HALF && r.c < rv) r.b = __ldcs(r.src + rv);
-    return r;
+  const int rv = HALF ? half / N : p.rot / N;   // vectors of a head that are turned
+  const int tok = threadIdx.z, c = threadIdx.x, n = blockIdx.x * p.tpc + tok;
+  const bool live = n < p.n_pos, rot = c < rv;
+  const int nq = p.jq * p.Hq, nh = nq + p.jk * p.Hk;  // the position's heads: rows n, n + n_pos, ... of q, then of k
+  // a pass-through vector c >= rv lies rv further on in "half"
+  const int v = rot ? c : c + (HALF ? rv : 0);
+  auto at = [&](int hh) {                       // element offset of the vector in q (hh < nq) or k
+    const bool isq = hh < nq;
+    if (!isq) hh -= nq;
+    const int H = isq ? p.Hq : p.Hk, J = isq ? p.jq : p.jk;
+    const int j = J == 1 ? 0 : hh / H;
+    return (((size_t)j * p.n_pos + n) * H + (hh - j * H)) * p.d + (size_t)(v * N);
   };
-  auto turn = [&](const RopeUnit& r) {
-    if (!r.src) return;
-    if (r.c >= rv) {  // behind the rotated part: as it is
-      __stcs(r.dst, r.a);
-      return;
-    }
-    float x[N], y[N];
-    if (HALF) {
-      Vec16<T>::unpack(r.a, x);
-      Vec16<T>::unpack(r.b, y);
+  uint4 a[kHeads], b[kHeads];
+  auto fetch = [&](int h0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float2 cs = tab[r.tok][r.c * N + i];
-        const float x1 = x[i], x2 = y[i];
-        x[i] = x1 * cs.x - x2 * cs.y;
-        y[i] = x2 * cs.x + x1 * cs.y;
-      }
-      __stcs(r.dst, Vec16<T>::pack(x));
-      __stcs(r.dst + rv, Vec16<T>::pack(y));
-    } else {
-      Vec16<T>::unpack(r.a, x);
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 cs = tab[r.tok][(r.c * N + i) / 2];
-        const float x1 = x[i], x2 = x[i + 1];
-        x[i] = x1 * cs.x - x2 * cs.y;
-        x[i + 1] = x2 * cs.x + x1 * cs.y;
-      }
-      __stcs(r.dst, Vec16<T>::pack(x));
+    for (int k = 0; k < kHeads; ++k) {
+      const int hh = h0 + k * blockDim.y;
+      if (!live || hh >= nh) continue;
+      const uint4* s = reinterpret_cast<const uint4*>(static_cast<const T*>(hh < nq ? p.q : p.k) + at(hh));
+      a[k] = __ldcs(s);
+      if (HALF && rot) b[k] = __ldcs(s + rv);
     }
   };
-
-  int u = threadIdx.x;
-  RopeUnit r0 = locate(u), r1 = locate(u + nt);
-  for (int i = threadIdx.x; i < ntok * half; i += nt) {
+  int h0 = threadIdx.y;
+  fetch(h0);
+  const int nt = blockDim.x * blockDim.y * blockDim.z, me = threadIdx.x + blockDim.x * (threadIdx.y + blockDim.y * threadIdx.z);
+  const int ntok = min(p.tpc, p.n_pos - (int)blockIdx.x * p.tpc);
+  for (int i = me; i < ntok * half; i += nt) {
     const int t = i / half, f = i - t * half;
-    double a = (double)p.pos[n0 + t] * p.turns[f];
-    a -= rint(a);                              // turns, in [-1/2, 1/2]
-    float s, c;
-    sincospif((float)(2.0 * a), &s, &c);
-    tab[t][f] = make_float2(c * p.mscale, s * p.mscale * p.sign);
+    double x = (double)p.pos[blockIdx.x * p.tpc + t] * p.turns[f];
+    x -= rint(x);                              // turns, in [-1/2, 1/2]
+    float sn, cs;
+    sincospif((float)(2.0 * x), &sn, &cs);
+    tab[t][f] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
   }
   __syncthreads();
-  while (r0.src) {
-    turn(r0);
-    turn(r1);
-    u += 2 * nt;
-    r0 = locate(u);
-    r1 = locate(u + nt);
+  if (!live) return;
+  float2 cs[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) cs[i] = rot ? tab[tok][c * NC + i] : make_float2(1.f, 0.f);
+  while (h0 < nh) {
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int hh = h0 + k * blockDim.y;
+      if (hh >= nh) continue;
+      uint4* d = reinterpret_cast<uint4*>(static_cast<T*>(hh < nq ? p.q_out : p.k_out) + at(hh));
+      if (!rot) {  // behind the rotated part: as it is
+        __stcs(d, a[k]);
+        continue;
+      }
+      float x[N];
+      Vec16<T>::unpack(a[k], x);
+      if constexpr (HALF) {
+        float y[N];
+        Vec16<T>::unpack(b[k], y);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float x1 = x[i], x2 = y[i];
+          x[i] = x1 * cs[i].x - x2 * cs[i].y;
+          y[i] = x2 * cs[i].x + x1 * cs[i].y;
+        }
+        __stcs(d, Vec16<T>::pack(x));
+        __stcs(d + rv, Vec16<T>::pack(y));
+      } else {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const float x1 = x[2 * i], x2 = x[2 * i + 1];
+          x[2 * i] = x1 * cs[i].x - x2 * cs[i].y;
+          x[2 * i + 1] = x2 * cs[i].x + x1 * cs[i].y;
+        }
+        __stcs(d, Vec16<T>::pack(x));
+      }
+    }
+    h0 += kHeads * blockDim.y;
+    fetch(h0);
   }
 }
 
@@ -215,22 +211,28 @@ cudaError_t launch_rope(const clsa_rope_args* a, cudaStream_t s) {
   p.sign = a->inverse ? -1.f : 1.f;
   const int n = a->dtype == CLSA_BF16 ? 8 : 4;
   const bool half = a->layout == CLSA_ROPE_HALF;
-  p.uph = (half ? a->rot / 2 : a->rot) / n + (a->d - a->rot) / n;
-  p.upt = (p.jq * p.Hq + p.jk * p.Hk) * p.uph;
-  // a CTA takes about 512 units (two a thread), more than one token where a token has few,
-  // but no more than spread n_pos over the SMs
-  const int spread = std::max(1, (a->n_pos + device_info().sm_count - 1) / std::max(1, device_info().sm_count));
-  p.tpc = std::max(1, std::min({kMaxTokRope, 512 / std::max(1, p.upt), spread}));
-  const int per = std::min(p.tpc * (long long)p.upt, 2LL * kMaxThreadsRope);
-  const int threads = std::min(kMaxThreadsRope, std::max(64, ((per + 1) / 2 + 31) / 32 * 32));
+  const int uph = (half ? a->rot / 2 : a->rot) / n + (a->d - a->rot) / n;  // vectors (or pairs of them) of a head: 4 to 32
+  const int nh = p.jq * p.Hq + p.jk * p.Hk;
+  // Many positions: up to kHeads heads a thread, in whole warps (100.8 us for 32768 x 40 heads; 105.5
+  // with 4 heads a thread, 80 threads a CTA; 150 with one).  Few: more threads, two heads each
+  // (2.3 us for 16 x 40 heads; 3.1 with five).
+  const bool many = a->n_pos >= 4 * device_info().sm_count;
+  int fit = 1;
+  while (fit < 32 && uph * fit % 32 != 0) fit *= 2;  // heads side by side that fill whole warps
+  int hy = many ? (nh + kHeads - 1) / kHeads : (nh + 1) / 2;
+  if (many) hy = (hy + fit - 1) / fit * fit;
+  hy = std::max(1, std::min({hy, nh, kMaxThreadsRope / uph}));
+  const int spread = std::max(1, a->n_pos / (4 * std::max(1, device_info().sm_count)));
+  p.tpc = std::max(1, std::min({kMaxTokRope, 128 / (uph * hy), spread}));
+  const dim3 threads(uph, hy, p.tpc);
   const dim3 grid((a->n_pos + p.tpc - 1) / p.tpc);
   cudaError_t e;
   if (a->dtype == CLSA_BF16)
-    e = half ? launch_pdl(rope_kernel<__nv_bfloat16, true>, grid, dim3(threads), 0, s, p)
-             : launch_pdl(rope_kernel<__nv_bfloat16, false>, grid, dim3(threads), 0, s, p);
+    e = half ? launch_pdl(rope_kernel<__nv_bfloat16, true>, grid, threads, 0, s, p)
+             : launch_pdl(rope_kernel<__nv_bfloat16, false>, grid, threads, 0, s, p);
   else
-    e = half ? launch_pdl(rope_kernel<float, true>, grid, dim3(threads), 0, s, p)
-             : launch_pdl(rope_kernel<float, false>, grid, dim3(threads), 0, s, p);
+    e = half ? launch_pdl(rope_kernel<float, true>, grid, threads, 0, s, p)
+             : launch_pdl(rope_kernel<float, false>, grid, threads, 0, s, p);
   launches_add(1, s);
   return e;
 }

@@ -1,4 +1,7 @@
-// Attention with a sliding window and sink tokens.
+// Attention with a sliding window and sink tokens: few rows stream over the cache (stream_attn.cuh), many run
+// in row tiles on tcgen05 (window_tc.cu).  fp32 always streams.
+#include <cmath>
+
 #include "stream_attn.cuh"
 
 namespace clsa {
@@ -40,11 +43,19 @@ auto dispatch(const clsa_window_args* a, int R, F&& f) {
   return d128 ? f(Cfg<kBf16, false, true, 128, 2>{}) : f(Cfg<kBf16, false, true, 64, 2>{});
 }
 
-// chunks with more rows per KV head than this run in row tiles of 128 on tcgen05
-constexpr long long kStreamRows = 64;
-
+// Which form is faster, by a fit to both over T = 8 to 512, windows 256 to 8192, 1 to 4 sequences and five
+// head layouts (d = 128, us): the streaming form takes 10 + 1.6e-3 per (16 rows, 16 tokens), at
+// 75 to 105 TFLOP/s whatever the split; the tcgen05 form 9.5 + 1.55 per token tile and round of the
+// SMs, since few rows leave most SMs idle.  E.g. T = 24, window 8192: 39 and 98; T = 96: 133 and 110;
+// T = 48, window 256: 10 and 14; T = 512, window 1024: 125 and 25.
 bool use_tc(const clsa_window_args* a) {
-  return (long long)a->T * (a->Hq / a->Hkv) > kStreamRows && window_tc_supported(a);
+  if (!window_tc_supported(a) || (long long)a->T * (a->Hq / a->Hkv) <= 16) return false;  // 16 rows: HBM is the bound
+  const double G = a->Hq / a->Hkv, TQ = 128 / (a->Hq / a->Hkv), sms = std::max(1, device_info().sm_count);
+  const double seen = std::min((double)a->n_max, (double)a->window + a->sinks);  // of one row
+  const double groups = std::ceil(a->T * G / 16) * a->B * a->Hkv, items = std::ceil(a->T / (2 * TQ)) * a->B * a->Hkv;
+  const double stream_us = 10 + 1.6e-3 * (a->d / 128.0) * groups * std::ceil((seen + 15) / 16) * (148 / sms);
+  const double tc_us = 9.5 + 1.55 * std::ceil(items / sms) * std::ceil(std::min((double)a->n_max, seen + 2 * TQ) / 128);
+  return tc_us < stream_us;
 }
 
 }  // namespace
