@@ -164,11 +164,14 @@ __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0x
 template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
 
-// A variant: the kind of cache, fp32 rows, tiles through the ring, head dimension, row tiles.
-template <int CACHE_, bool F32_, bool RING_, int D_, int NT_>
+// How tiles come: plain loads into registers, or through the warp's ring, by TMA (consecutive tokens) or
+// by 16-byte asynchronous copies (an index list's).
+enum Feed { kLoads = 0, kTma = 1, kGather = 2 };
+// A variant: the kind of cache, fp32 rows, the feed, head dimension, row tiles.
+template <int CACHE_, bool F32_, int FEED_, int D_, int NT_>
 struct Cfg {
-  static constexpr int CACHE = CACHE_, D = D_, NT = NT_;
-  static constexpr bool F32 = F32_, RING = RING_;
+  static constexpr int CACHE = CACHE_, FEED = FEED_, D = D_, NT = NT_;
+  static constexpr bool F32 = F32_, RING = FEED_ != kLoads;
   static constexpr int ROWS = NT * 8;
   static constexpr int ES = CACHE == kE4m3 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
   static constexpr int RB = D * ES;                                       // bytes of a token's row
@@ -176,7 +179,10 @@ struct Cfg {
   // warps of a CTA (one CTA per SM): what the registers allow.  One large CTA rather than
   // three small: a unit that all SMs share has a third of the partials to merge.
   static constexpr int W = RING ? (NT == 2 ? 8 : 12) : (NT == 1 && CACHE != kFp32 ? 12 : 8);
-  static constexpr int NST = RING ? (192 * 1024 / (W * STAGE) < 6 ? 192 * 1024 / (W * STAGE) : 6) : 1;  // ring tiles of a warp
+  // ring tiles of a warp: three of consecutive tokens are enough (51.0 us over 128K tokens with three, 53.0 with
+  // four, 50.8 with two); of an index list as many as there is room for, up to six
+  static constexpr int ROOM = 192 * 1024 / (W * STAGE), MOST = FEED == kGather ? 6 : 3;
+  static constexpr int NST = RING ? (ROOM < MOST ? ROOM : MOST) : 1;
   // dynamic shared memory: the ring; over it the warps' outputs, or the weights of P contributors
   static size_t smem(int P) {
     return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 4}) + 1024;
@@ -186,9 +192,10 @@ struct Cfg {
 template <typename C>
 __device__ void kernel_body(const Maps& maps, const Params& p) {
   constexpr int CACHE = C::CACHE, D = C::D, NT = C::NT, ROWS = C::ROWS, ES = C::ES, RB = C::RB, NST = C::NST;
-  constexpr bool F32 = C::F32, RING = C::RING, FP8 = CACHE == kE4m3;
+  constexpr bool F32 = C::F32, RING = C::RING, GATHER = C::FEED == kGather, TMA = C::FEED == kTma, FP8 = CACHE == kE4m3;
   static_assert(F32 ? CACHE != kBf16 : CACHE != kFp32, "bf16 cache: bf16 rows; fp32 cache: fp32 rows");
   static_assert(!RING || NST >= 2, "a ring of two tiles at least");
+  static_assert(GATHER ? FP8 : !FP8 || TMA, "index lists: the 8-bit cache, through the ring");
   constexpr int kWarps = C::W, kThreads = kWarps * 32;
   constexpr int KC = D * ES / 64;              // 16-byte chunks of a token's row that a lane takes
   constexpr int KS = D / 16;                   // k steps of S, d tiles of O
@@ -201,7 +208,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* const sm_base = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   float* const sm_o = reinterpret_cast<float*>(sm_base);
-  __shared__ uint64_t sm_full[RING ? kWarps : 1][RING ? NST : 1];
+  __shared__ uint64_t sm_full[TMA ? kWarps : 1][NST];
   __shared__ float sm_m[3][kWarps][ROWS];
   __shared__ float sm_w[kWarps][ROWS];         // the warps' weights
   __shared__ float sm_f[ROWS];
@@ -213,7 +220,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int nS = p.B * p.nrg, c = blockIdx.x;
-  if (RING && lane == 0) {                     // the warp's own barriers
+  if (TMA && lane == 0) {                      // the warp's own barriers
 #pragma unroll
     for (int i = 0; i < NST; ++i) mbar_init(&sm_full[warp][i], 1);
     fence_mbar_init();
@@ -387,13 +394,18 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     auto token = [&](int t) {
       const int i = t * kTile + (lane & 15);
       if (t >= t_end || i >= it.npos) return -1;
-      if (!RING && FP8) {
+      if (GATHER) {
         const int tk = __ldg(p.idx + (size_t)b * p.k + i);
         if ((unsigned)tk < (unsigned)p.n_max) return tk;
         if (lane < 16) record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)i);
         return -1;
       }
       return FP8 ? i : token_of(it, i);
+    };
+    // byte offset of 16-byte chunk ch of token r's row in a stage (ch counts through the row)
+    auto chunk = [&](int r, int ch) {
+      if constexpr (RB == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+      else return (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
     };
     // the ring: tile t by TMA, 128 bytes of 16 tokens a box, swizzled by the TMA unit
     auto issue = [&](int t) {
@@ -412,10 +424,23 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       ++issued;
     };
-    // byte offset of 16-byte chunk ch of token r's row in a stage (ch counts through the row)
-    auto chunk = [&](int r, int ch) {
-      if constexpr (RB == 64) return r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
-      else return (ch >> 3) * 2048 + r * 128 + (((ch & 7) ^ (r & 7)) << 4);
+    // ... or by 16-byte copies of the tile's tokens (lane l holds token l % 16's row; none: zeros); a commit
+    // group a tile, so that groups count tiles
+    auto gather = [&](int t, int tok) {
+      if (t < t_end) {
+        unsigned char* dst = ring + (issued % NST) * C::STAGE;
+        constexpr int CH = RB / 16;
+#pragma unroll
+        for (int i = 0; i < kTile * CH / 32; ++i) {
+          const int r = (lane + 32 * i) / CH, ch = (lane + 32 * i) % CH;
+          const int tk = __shfl_sync(0xffffffffu, tok, r);
+          const size_t off = tk >= 0 ? (size_t)tk * rstr + 16 * ch : 0;
+          cp_async_16(dst + chunk(r, ch), kb + off, tk >= 0 ? 16 : 0);
+          cp_async_16(dst + kTile * RB + chunk(r, ch), vb + off, tk >= 0 ? 16 : 0);
+        }
+        ++issued;
+      }
+      cp_async_commit();
     };
     uint4 kr[2][KC];                             // K: tokens gid, gid + 8
     VecV vr[4][VC];                              // V: tokens 2 tig, 2 tig + 1, + 8, + 9
@@ -514,10 +539,20 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     const int nw = min(kWarps, t_end - t_beg);   // warps that have a tile
     int t = t_beg + warp, tok = -1, tok_n = -1;
     float sc;
-    if constexpr (RING) {
+    int tok_g = -1;                              // gather: tokens of the next tile to be issued
+    if constexpr (TMA) {
 #pragma unroll
       for (int x = 0; x < NST; ++x) issue(t + x * kWarps);
       tok = token(t);
+      sc = load_scale(tok);
+    } else if constexpr (GATHER) {
+      int tk[NST];
+#pragma unroll
+      for (int x = 0; x < NST; ++x) tk[x] = token(t + x * kWarps);
+      tok_g = token(t + NST * kWarps);
+#pragma unroll
+      for (int x = 0; x < NST; ++x) gather(t + x * kWarps, tk[x]);
+      tok = tk[0];
       sc = load_scale(tok);
     } else {
       tok = token(t);
@@ -534,7 +569,10 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       unsigned char* stage = nullptr;
       if constexpr (RING) {
         const int slot = used % NST;
-        if (!dead && !mbar_wait_warp(&sm_full[warp][slot], (uint32_t)(used / NST) & 1u)) {
+        if constexpr (GATHER) {
+          cp_async_wait<NST - 1>();
+          __syncwarp();
+        } else if (!dead && !mbar_wait_warp(&sm_full[warp][slot], (uint32_t)(used / NST) & 1u)) {
           if (lane == 0) record_error(p.ws_header, CLSA_ERR_TIMEOUT, 70);
           dead = true;
         }
@@ -601,7 +639,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
           }
         }
         // a tile with places that hold no token of the unit: whatever lies there, V = 0
-        if (!__all_sync(0xffffffffu, tok >= 0)) {
+        if (TMA && !__all_sync(0xffffffffu, tok >= 0)) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int tk = __shfl_sync(0xffffffffu, tok, 2 * tig + (h & 1) + 8 * (h >> 1));
@@ -750,7 +788,12 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       if constexpr (RING) {
         __syncwarp();                            // the stage has been used: the next tile may overwrite it
-        issue(t + NST * kWarps);
+        if constexpr (GATHER) {
+          gather(t + NST * kWarps, tok_g);
+          tok_g = token(t + (NST + 1) * kWarps);
+        } else {
+          issue(t + NST * kWarps);
+        }
       } else {
         load_v(tok_n);
       }
@@ -758,6 +801,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       tok_n = tok_nn;
     }
     if constexpr (RING) {
+      if (GATHER) cp_async_wait<0>();
       if (dead) {                                // loads in flight land before their memory has another use
         for (; used < issued; ++used) mbar_wait_warp(&sm_full[warp][used % NST], (uint32_t)(used / NST) & 1u);
       }
@@ -954,7 +998,7 @@ cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   p.counter = static_cast<uint32_t*>(ws_body);
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
   Maps maps{};
-  if (C::RING) {
+  if (C::FEED == kTma) {
     const uint64_t rows = (uint64_t)p.seqs * p.n_max, bytes = (uint64_t)p.Hkv * C::RB;
     if (!make_map(&maps.k, p.K, rows, bytes, std::min(C::RB, 128)) || !make_map(&maps.v, p.V, rows, bytes, std::min(C::RB, 128)))
       return cudaErrorInvalidValue;
