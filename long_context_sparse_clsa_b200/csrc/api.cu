@@ -117,6 +117,7 @@ clsa_status check_kv8(const clsa_kv8_cache* c) {
 
 // sizes that the streaming attention counts in 32 bits: rows of a KV head, (sequence, row) pairs
 constexpr long long kMaxStreamRows = 1LL << 24;
+constexpr long long kMaxCacheRows = (1LL << 31) - 4096;  // rows of a cache: what the TMA coordinates reach
 
 clsa_status check_kv8_attn(const clsa_kv8_attn_args* a) {
   if (!a) return CLSA_ERR_INVALID_ARG;
@@ -131,6 +132,7 @@ clsa_status check_kv8_attn(const clsa_kv8_attn_args* a) {
   // tiles of 16 tokens over all (sequence, 8 rows, KV head) units
   const long long G = a->Hq / a->cache.Hkv, n = a->idx ? a->k : a->cache.n_max;
   if ((double)a->B * ((a->L * G + 7) / 8) * a->cache.Hkv * ((n + 15) / 16) > 2e9) return CLSA_ERR_UNSUPPORTED;
+  if ((long long)a->cache.B * a->cache.n_max > kMaxCacheRows) return CLSA_ERR_UNSUPPORTED;
   if (!aligned16(a->Q) || !aligned16(a->O)) return CLSA_ERR_INVALID_ARG;
   for (const void* p : {(const void*)a->idx, (const void*)a->count, (const void*)a->lse})
     if (p && !aligned4(p)) return CLSA_ERR_INVALID_ARG;
@@ -149,6 +151,7 @@ clsa_status check_window(const clsa_window_args* a) {
   // tiles of 16 tokens over all (sequence, 8 rows, KV head) units
   const double seen = std::min((double)a->n_max, (double)a->window + a->sinks + 16.0), G = a->Hq / a->Hkv;
   if (a->B * std::ceil(a->T * G / 8) * a->Hkv * std::ceil(seen / 16 + 1) > 2e9) return CLSA_ERR_UNSUPPORTED;
+  if ((long long)a->B * a->n_max > kMaxCacheRows) return CLSA_ERR_UNSUPPORTED;
   for (const void* p : {a->Q, a->K, a->V, (const void*)a->O})
     if (!aligned16(p)) return CLSA_ERR_INVALID_ARG;
   if (!aligned4(a->seq_lens) || (a->lse && !aligned4(a->lse))) return CLSA_ERR_INVALID_ARG;

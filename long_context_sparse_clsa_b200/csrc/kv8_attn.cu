@@ -36,15 +36,15 @@ stream::Params params_of(const clsa_kv8_attn_args* a, float scale) {
 }
 
 // calls f<Cfg>
-template <int FEED, typename F>
+template <bool RING, typename F>
 auto dispatch(const clsa_kv8_attn_args* a, int R, F&& f) {
   using namespace stream;
   const bool d128 = a->cache.d == 128;
   if (a->dtype == CLSA_F32)
-    return d128 ? f(Cfg<kE4m3, true, FEED, 128, 1>{}) : f(Cfg<kE4m3, true, FEED, 64, 1>{});
+    return d128 ? f(Cfg<kE4m3, true, RING, 128, 1>{}) : f(Cfg<kE4m3, true, RING, 64, 1>{});
   if (row_tiles(R, false) == 1)
-    return d128 ? f(Cfg<kE4m3, false, FEED, 128, 1>{}) : f(Cfg<kE4m3, false, FEED, 64, 1>{});
-  return d128 ? f(Cfg<kE4m3, false, FEED, 128, 2>{}) : f(Cfg<kE4m3, false, FEED, 64, 2>{});
+    return d128 ? f(Cfg<kE4m3, false, RING, 128, 1>{}) : f(Cfg<kE4m3, false, RING, 64, 1>{});
+  return d128 ? f(Cfg<kE4m3, false, RING, 128, 2>{}) : f(Cfg<kE4m3, false, RING, 64, 2>{});
 }
 
 }  // namespace
@@ -52,14 +52,14 @@ auto dispatch(const clsa_kv8_attn_args* a, int R, F&& f) {
 size_t kv8_attn_ws_bytes(const clsa_kv8_attn_args* a) {
   const stream::Params p = params_of(a, 1.f);
   const auto f = [&](auto c) { return stream::ws_bytes<decltype(c)>(p); };
-  return a->idx ? dispatch<stream::kGather>(a, p.R, f) : dispatch<stream::kTma>(a, p.R, f);
+  return a->idx ? dispatch<false>(a, p.R, f) : dispatch<true>(a, p.R, f);
 }
 
 cudaError_t launch_kv8_attn(const clsa_kv8_attn_args* a, float scale, void* ws_header, void* ws_body, cudaStream_t s) {
   stream::Params p = params_of(a, scale);
   p.ws_header = ws_header;
   const auto f = [&](auto c) { return stream::launch<decltype(c)>(p, ws_body, s); };
-  return a->idx ? dispatch<stream::kGather>(a, p.R, f) : dispatch<stream::kTma>(a, p.R, f);
+  return a->idx ? dispatch<false>(a, p.R, f) : dispatch<true>(a, p.R, f);
 }
 
 }  // namespace clsa

@@ -50,7 +50,6 @@ namespace stream {
 
 constexpr int kTile = 16;                   // tokens of a tile
 constexpr int kMinTiles = 12;               // fewest tiles worth a CTA (one a warp)
-constexpr int kAhead = 4;                   // tiles of a warp between its L2 prefetch and its loads
 constexpr float kNone = -3e38f;             // reference of a row that has seen nothing
 constexpr float kTau = 8.f;
 constexpr float kLift = 7.f;                // 8-bit cache: the largest p of a row lies in [2^7, 2^15] of half range
@@ -72,6 +71,7 @@ struct Params {
   void* ws_header;
   long long q_sl, q_sb;
   int B, nrg, R, Hkv, G, n_max, k, nblk, bshift, seqs;
+  int HG, nh, PG;           // heads side by side, Hkv / HG, groups of HG CTAs
   int T, window, sinks;     // T > 0: row r is the token count - T + r / G and sees a window and the sinks
   float scale_log2;
 };
@@ -88,7 +88,7 @@ struct Item {
 
 __device__ __forceinline__ Item item_of(const Params& p, int s, int rows) {
   Item it;
-  it.b = s / p.nrg;
+  it.b = p.nrg == 1 ? s : s / p.nrg;
   it.rg = s - it.b * p.nrg;
   const int cnt = p.count[it.b];
   it.p0 = 0;
@@ -112,6 +112,14 @@ __device__ __forceinline__ Item item_of(const Params& p, int s, int rows) {
   it.npos = it.keepP + last + 1 - lo;
   return it;
 }
+__device__ __forceinline__ Item item_from(const Item& x, int lane) {  // a lane's item, to all
+  Item it;
+  it.b = __shfl_sync(0xffffffffu, x.b, lane), it.rg = __shfl_sync(0xffffffffu, x.rg, lane);
+  it.npos = __shfl_sync(0xffffffffu, x.npos, lane), it.p0 = __shfl_sync(0xffffffffu, x.p0, lane);
+  it.keep = __shfl_sync(0xffffffffu, x.keep, lane), it.keepP = __shfl_sync(0xffffffffu, x.keepP, lane);
+  it.shift = __shfl_sync(0xffffffffu, x.shift, lane);
+  return it;
+}
 __device__ __forceinline__ int token_of(const Item& it, int i) {  // token of position i, or -1
   return i >= it.npos ? -1 : i >= it.keepP ? i + it.shift : i < it.keep ? i : -1;
 }
@@ -122,6 +130,9 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], const uint32_t (&a)
       "{%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void prefetch_tensormap(const CUtensorMap* m) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   uint32_t r;
@@ -164,14 +175,12 @@ __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0x
 template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
 
-// How tiles come: plain loads into registers, or through the warp's ring, by TMA (consecutive tokens) or
-// by 16-byte asynchronous copies (an index list's).
-enum Feed { kLoads = 0, kTma = 1, kGather = 2 };
-// A variant: the kind of cache, fp32 rows, the feed, head dimension, row tiles.
-template <int CACHE_, bool F32_, int FEED_, int D_, int NT_>
+// A variant: the kind of cache, fp32 rows, consecutive tokens through the ring (or loads into registers), head
+// dimension, row tiles.
+template <int CACHE_, bool F32_, bool RING_, int D_, int NT_>
 struct Cfg {
-  static constexpr int CACHE = CACHE_, FEED = FEED_, D = D_, NT = NT_;
-  static constexpr bool F32 = F32_, RING = FEED_ != kLoads;
+  static constexpr int CACHE = CACHE_, D = D_, NT = NT_;
+  static constexpr bool F32 = F32_, RING = RING_;
   static constexpr int ROWS = NT * 8;
   static constexpr int ES = CACHE == kE4m3 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
   static constexpr int RB = D * ES;                                       // bytes of a token's row
@@ -179,23 +188,22 @@ struct Cfg {
   // warps of a CTA (one CTA per SM): what the registers allow.  One large CTA rather than
   // three small: a unit that all SMs share has a third of the partials to merge.
   static constexpr int W = RING ? (NT == 2 ? 8 : 12) : (NT == 1 && CACHE != kFp32 ? 12 : 8);
-  // ring tiles of a warp: three of consecutive tokens are enough (51.0 us over 128K tokens with three, 53.0 with
-  // four, 50.8 with two); of an index list as many as there is room for, up to six
-  static constexpr int ROOM = 192 * 1024 / (W * STAGE), MOST = FEED == kGather ? 6 : 3;
-  static constexpr int NST = RING ? (ROOM < MOST ? ROOM : MOST) : 1;
-  // dynamic shared memory: the ring; over it the warps' outputs, or the weights of P contributors
+  // ring tiles of a warp: three (50.8 us over 128K tokens; 53.0 with four, 51.0 with two), or what there is room for
+  static constexpr int ROOM = 192 * 1024 / (W * STAGE);
+  static constexpr int NST = RING ? (ROOM < 3 ? ROOM : 3) : 1;
+  // dynamic shared memory: the ring; over it the warps' outputs, or the statistics of P contributors and
+  // their outputs' sums
   static size_t smem(int P) {
-    return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 4}) + 1024;
+    return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 12 + W * 32 * 16}) + 1024;
   }
 };
 
 template <typename C>
 __device__ void kernel_body(const Maps& maps, const Params& p) {
   constexpr int CACHE = C::CACHE, D = C::D, NT = C::NT, ROWS = C::ROWS, ES = C::ES, RB = C::RB, NST = C::NST;
-  constexpr bool F32 = C::F32, RING = C::RING, GATHER = C::FEED == kGather, TMA = C::FEED == kTma, FP8 = CACHE == kE4m3;
+  constexpr bool F32 = C::F32, RING = C::RING, FP8 = CACHE == kE4m3, IDX = FP8 && !RING;
   static_assert(F32 ? CACHE != kBf16 : CACHE != kFp32, "bf16 cache: bf16 rows; fp32 cache: fp32 rows");
   static_assert(!RING || NST >= 2, "a ring of two tiles at least");
-  static_assert(GATHER ? FP8 : !FP8 || TMA, "index lists: the 8-bit cache, through the ring");
   constexpr int kWarps = C::W, kThreads = kWarps * 32;
   constexpr int KC = D * ES / 64;              // 16-byte chunks of a token's row that a lane takes
   constexpr int KS = D / 16;                   // k steps of S, d tiles of O
@@ -208,9 +216,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   extern __shared__ __align__(1024) unsigned char sm_raw[];
   unsigned char* const sm_base = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
   float* const sm_o = reinterpret_cast<float*>(sm_base);
-  __shared__ uint64_t sm_full[TMA ? kWarps : 1][NST];
+  __shared__ uint64_t sm_full[RING ? kWarps : 1][NST];
   __shared__ float sm_m[3][kWarps][ROWS];
-  __shared__ float sm_w[kWarps][ROWS];         // the warps' weights
   __shared__ float sm_f[ROWS];
   __shared__ long long sm_off[ROWS];           // where the unit's rows lie in Q and O
   __shared__ int sm_scan[kWarps];
@@ -220,7 +227,11 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int nS = p.B * p.nrg, c = blockIdx.x;
-  if (TMA && lane == 0) {                      // the warp's own barriers
+  if (RING && lane == 0) {                     // the warp's own barriers
+    if (warp == 0) {
+      prefetch_tensormap(&maps.k);
+      prefetch_tensormap(&maps.v);
+    }
 #pragma unroll
     for (int i = 0; i < NST; ++i) mbar_init(&sm_full[warp][i], 1);
     fence_mbar_init();
@@ -251,11 +262,9 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     }
   }
 
-  // Heads together: CTAs c, c + 1, ... take the heads of the same tokens, so that the cache's rows, which
-  // hold all heads, are read whole at about the same time.  Only where few CTAs stay idle for it.
-  const bool folded = p.Hkv <= (int)gridDim.x && (gridDim.x % p.Hkv) * 16 <= gridDim.x;
-  const int HG = folded ? p.Hkv : 1, nh = p.Hkv / HG;  // heads side by side, heads in the line
-  const int PG = gridDim.x / HG, cg = c / HG, gsub = c - cg * HG;
+  // CTAs c, c + 1, ... take the HG heads of the same tokens; nh heads are in the line
+  const int HG = p.HG, nh = p.nh, PG = p.PG, cg = HG == 1 ? c : c / HG, gsub = c - cg * HG;
+  const bool folded = nh == 1;
   const int nU = nS * nh;
   if (cg >= PG) return;
   // Two ways to share.  Whole CTAs per unit (a unit of x of all N tiles takes x PG / N of them): no CTA
@@ -268,20 +277,28 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   int N, P, q, rem;                              // CTA cc takes tiles [bnd(cc), bnd(cc + 1)) of N
   auto bnd = [&](int cc) { return cc * q + min(cc, rem); };
   auto owner = [&](int t) { return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q; };
+  Item it;
   if (nU <= 32) {                                // every warp for itself, a lane per unit
-    const int mine = lane < nU ? tiles_of(item_of(p, lane / nh, ROWS).npos) : 0;
+    it.npos = 0;
+    if (lane < nU) it = item_of(p, folded ? lane : lane / nh, ROWS);
+    const int mine = tiles_of(it.npos);
     N = warp_sum_int(mine);
     if (N == 0) return;
-    const int fair = mine < (1 << 24) ? (int)((unsigned)mine * (unsigned)PG / (unsigned)N) : mine / ((N + PG - 1) / PG);
+    // floor(mine PG / N): a quotient of floats is off by one at most
+    int fair = (int)__fdividef((float)mine * PG, (float)N);
+    const long long off = (long long)mine * PG - (long long)fair * N;
+    fair += off < 0 ? -1 : off >= N ? 1 : 0;
     const int want = mine > 0 ? max(1, min(fair, (mine + kMinTiles - 1) / kMinTiles)) : 0;
-    const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(want > 0 ? (mine + want - 1) / want : 0));
+    const int most = (int)__reduce_max_sync(0xffffffffu, want > 0 ? (unsigned)ceilf(__fdividef((float)mine, (float)want)) : 0u);
     const int pref = warp_scan_int(want, lane) - want, used = __shfl_sync(0xffffffffu, pref + want, 31);
-    whole = used <= PG && most <= N / PG + N / PG / 8 + 2 * kWarps;
+    const float share = __fdividef((float)N, (float)PG);
+    whole = used <= PG && most <= (int)(share * 1.125f) + 2 * kWarps;
+    int u;
     if (whole) {
       const unsigned here = __ballot_sync(0xffffffffu, pref <= cg && cg < pref + want);
       if (here == 0) return;                     // more CTAs than wanted
-      const int u = __ffs(here) - 1;
-      s = u / nh;
+      u = __ffs(here) - 1;
+      s = folded ? u : u / nh;
       u_g = u - s * nh;
       u_c0 = __shfl_sync(0xffffffffu, pref, u);
       u_n = __shfl_sync(0xffffffffu, want, u);
@@ -293,10 +310,11 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       r0 = bnd(cg);
       r1 = bnd(cg + 1);
       const int before = warp_scan_int(mine, lane) - mine;
-      const int u = __ffs(__ballot_sync(0xffffffffu, before <= r0 && r0 < before + mine)) - 1;
+      u = __ffs(__ballot_sync(0xffffffffu, before <= r0 && r0 < before + mine)) - 1;
       s = u / nh;
       base = __shfl_sync(0xffffffffu, before, s * nh);
     }
+    it = item_from(it, u);
   } else {                                       // a run of items per thread
     const int per = (nS + kThreads - 1) / kThreads;
     int mine = 0;
@@ -333,8 +351,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     __syncthreads();
     s = sm_unit[0];
     base = sm_unit[1];
+    it = item_of(p, s, ROWS);
   }
-  Item it = item_of(p, s, ROWS);
 
   while (r0 < r1) {
     // ---- the next unit (it, g): its tiles [t_beg, t_end); CTA groups c0 .. c0 + n - 1 share it -------
@@ -364,7 +382,6 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       r0 = min(r1, te);
     }
     const int b = it.b, row0 = it.rg * ROWS, nr = min(ROWS, p.R - row0);
-    if (tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
 
     float o[NT][KS][4], l[NT][2], m[NT][2], mv[NT][2];
 #pragma unroll
@@ -394,7 +411,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     auto token = [&](int t) {
       const int i = t * kTile + (lane & 15);
       if (t >= t_end || i >= it.npos) return -1;
-      if (GATHER) {
+      if (IDX) {
         const int tk = __ldg(p.idx + (size_t)b * p.k + i);
         if ((unsigned)tk < (unsigned)p.n_max) return tk;
         if (lane < 16) record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)i);
@@ -423,24 +440,6 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
         }
       }
       ++issued;
-    };
-    // ... or by 16-byte copies of the tile's tokens (lane l holds token l % 16's row; none: zeros); a commit
-    // group a tile, so that groups count tiles
-    auto gather = [&](int t, int tok) {
-      if (t < t_end) {
-        unsigned char* dst = ring + (issued % NST) * C::STAGE;
-        constexpr int CH = RB / 16;
-#pragma unroll
-        for (int i = 0; i < kTile * CH / 32; ++i) {
-          const int r = (lane + 32 * i) / CH, ch = (lane + 32 * i) % CH;
-          const int tk = __shfl_sync(0xffffffffu, tok, r);
-          const size_t off = tk >= 0 ? (size_t)tk * rstr + 16 * ch : 0;
-          cp_async_16(dst + chunk(r, ch), kb + off, tk >= 0 ? 16 : 0);
-          cp_async_16(dst + kTile * RB + chunk(r, ch), vb + off, tk >= 0 ? 16 : 0);
-        }
-        ++issued;
-      }
-      cp_async_commit();
     };
     uint4 kr[2][KC];                             // K: tokens gid, gid + 8
     VecV vr[4][VC];                              // V: tokens 2 tig, 2 tig + 1, + 8, + 9
@@ -539,20 +538,10 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     const int nw = min(kWarps, t_end - t_beg);   // warps that have a tile
     int t = t_beg + warp, tok = -1, tok_n = -1;
     float sc;
-    int tok_g = -1;                              // gather: tokens of the next tile to be issued
-    if constexpr (TMA) {
+    if constexpr (RING) {
 #pragma unroll
       for (int x = 0; x < NST; ++x) issue(t + x * kWarps);
       tok = token(t);
-      sc = load_scale(tok);
-    } else if constexpr (GATHER) {
-      int tk[NST];
-#pragma unroll
-      for (int x = 0; x < NST; ++x) tk[x] = token(t + x * kWarps);
-      tok_g = token(t + NST * kWarps);
-#pragma unroll
-      for (int x = 0; x < NST; ++x) gather(t + x * kWarps, tk[x]);
-      tok = tk[0];
       sc = load_scale(tok);
     } else {
       tok = token(t);
@@ -564,15 +553,13 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     if constexpr (FP8) {
       if (warp < nw) load_q();
     }
+    if (tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
     for (; t < t_end; t += kWarps) {
       int tok_nn = -1;
       unsigned char* stage = nullptr;
       if constexpr (RING) {
         const int slot = used % NST;
-        if constexpr (GATHER) {
-          cp_async_wait<NST - 1>();
-          __syncwarp();
-        } else if (!dead && !mbar_wait_warp(&sm_full[warp][slot], (uint32_t)(used / NST) & 1u)) {
+        if (!dead && !mbar_wait_warp(&sm_full[warp][slot], (uint32_t)(used / NST) & 1u)) {
           if (lane == 0) record_error(p.ws_header, CLSA_ERR_TIMEOUT, 70);
           dead = true;
         }
@@ -639,7 +626,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
           }
         }
         // a tile with places that hold no token of the unit: whatever lies there, V = 0
-        if (TMA && !__all_sync(0xffffffffu, tok >= 0)) {
+        if (!__all_sync(0xffffffffu, tok >= 0)) {
 #pragma unroll
           for (int h = 0; h < 4; ++h) {
             const int tk = __shfl_sync(0xffffffffu, tok, 2 * tig + (h & 1) + 8 * (h >> 1));
@@ -788,12 +775,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       if constexpr (RING) {
         __syncwarp();                            // the stage has been used: the next tile may overwrite it
-        if constexpr (GATHER) {
-          gather(t + NST * kWarps, tok_g);
-          tok_g = token(t + (NST + 1) * kWarps);
-        } else {
-          issue(t + NST * kWarps);
-        }
+        issue(t + NST * kWarps);
       } else {
         load_v(tok_n);
       }
@@ -801,7 +783,6 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       tok_n = tok_nn;
     }
     if constexpr (RING) {
-      if (GATHER) cp_async_wait<0>();
       if (dead) {                                // loads in flight land before their memory has another use
         for (; used < issued; ++used) mbar_wait_warp(&sm_full[warp][used % NST], (uint32_t)(used / NST) & 1u);
       }
@@ -835,30 +816,22 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
     }
     __syncthreads();
-    // a thread per (warp, row): the warp's weight; the first of a row: the row's references and sum
-    float M = kNone, Mv = kNone, L = 0.f;
-    if (tid < nw * ROWS) {
-      const int w0 = tid / ROWS, row = tid % ROWS;
+    // float4 i of the unit's rows over the warps, with its row's references and sum
+    auto warps_sum = [&](int i, float& M, float& Mv, float& L) {
+      const int row = i / (D / 4);
+      M = Mv = kNone;
 #pragma unroll 4
       for (int w = 0; w < nw; ++w) {
         M = fmaxf(M, sm_m[0][w][row]);
         Mv = fmaxf(Mv, sm_m[1][w][row]);
       }
-      sm_w[w0][row] = fast_exp2(sm_m[1][w0][row] - Mv);
-      if (w0 == 0) {
-#pragma unroll 4
-        for (int w = 0; w < nw; ++w) L += sm_m[2][w][row] * fast_exp2(sm_m[0][w][row] - M);
-        sm_f[row] = L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L;
-      }
-    }
-    __syncthreads();
-    auto warps_sum = [&](int i) {  // float4 i of the unit's rows, over the warps
-      const int row = i / (D / 4);
+      L = 0.f;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
       for (int w = 0; w < nw; ++w) {
         const float4 y = *so(w, row, i % (D / 4));
-        const float f = sm_w[w][row];
+        const float f = fast_exp2(sm_m[1][w][row] - Mv);
+        L += sm_m[2][w][row] * (FP8 ? fast_exp2(sm_m[0][w][row] - M) : f);
         x.x = fmaf(f, y.x, x.x);
         x.y = fmaf(f, y.y, x.y);
         x.z = fmaf(f, y.z, x.z);
@@ -866,18 +839,21 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       return x;
     };
+    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
     auto lse_of = [&](int row, float M, float L) {
       if (p.lse) p.lse[sm_off[row] / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     };
+    const int tasks = nr * (D / 4);              // float4s of the unit's rows
     if (n == 1) {
-      for (int i = tid; i < nr * (D / 4); i += kThreads) {
-        const int row = i / (D / 4);
-        const float f = sm_f[row];
-        float4 x = warps_sum(i);
+#pragma unroll 1
+      for (int i = tid; i < tasks; i += kThreads) {
+        float M, Mv, L;
+        float4 x = warps_sum(i, M, Mv, L);
+        const float f = over_sum(M, Mv, L);
         x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-        store4(sm_off[row] + (i % (D / 4)) * 4, x);
+        store4(sm_off[i / (D / 4)] + (i % (D / 4)) * 4, x);
+        if (i % (D / 4) == 0) lse_of(i / (D / 4), M, L);
       }
-      if (tid < nr) lse_of(tid, M, L);
       if (RING) fence_proxy_async_smem();        // before the next unit's TMA writes
       __syncthreads();                           // shared memory is free again
       continue;
@@ -888,65 +864,96 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     const int step = 2 * HG * slot_floats<D, NT>();
     const auto slot = [&](int i) { return part0 + (i * step + (i == 0 ? slot_floats<D, NT>() : 0)); };
     float* my = slot(cg - c0);
-    for (int i = tid; i < ROWS * (D / 4); i += kThreads) __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i));
-    if (tid < ROWS) {
-      __stcg(my + ROWS * D + tid, M);
-      __stcg(my + ROWS * (D + 1) + tid, Mv);
-      __stcg(my + ROWS * (D + 2) + tid, L);
+#pragma unroll 1
+    for (int i = tid; i < tasks; i += kThreads) {
+      float M, Mv, L;
+      __stcg(reinterpret_cast<float4*>(my) + i, warps_sum(i, M, Mv, L));
+      if (i % (D / 4) == 0) {
+        float* x = my + ROWS * D + i / (D / 4);
+        __stcg(x, M);
+        __stcg(x + ROWS, Mv);
+        __stcg(x + 2 * ROWS, L);
+      }
     }
     uint32_t* ctr = p.counter + (size_t)s * p.Hkv + g;
     __syncthreads();  // every thread's part is stored before the arrival, which releases them
     if (tid == 0) sm_last = atom_add_acq_rel_gpu(ctr, 1u) == (uint32_t)(n - 1);
     __syncthreads();
     if (sm_last) {      // the others' parts, released before their arrivals
-      constexpr int kB = 8;  // loads in flight
+      // S threads per float4, each for every S-th part, kB loads in flight
+      constexpr int kB = 8;
+      const int S = tasks < kThreads ? min(kThreads / tasks, n) : 1, sl = S > 1 ? tid / tasks : 0;
+      float* const st = sm_o;                    // [3][n ROWS]: references, output references or weights, sums
+      float4* const sums = reinterpret_cast<float4*>(sm_o + (3 * n * ROWS + 3) / 4 * 4);
       float4 y[kB];
       auto fetch = [&](int i, int j0) {
 #pragma unroll
-        for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(min(j0 + j, n - 1))) + i);
+        for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(min(j0 + j * S, n - 1))) + i);
       };
-      if (tid < nr * (D / 4)) fetch(tid, 0);
-      for (int row = warp; row < nr; row += kWarps) {
-        M = Mv = kNone;
-        L = 0.f;
-        for (int i = lane; i < n; i += 32) {
-          const float* x = slot(i) + ROWS * D + row;
-          const float mi = __ldcg(x), vi = __ldcg(x + ROWS), li = __ldcg(x + 2 * ROWS);
-          const float top = fmaxf(M, mi);
-          L = L * fast_exp2(M - top) + li * fast_exp2(mi - top);
-          M = top;
-          Mv = fmaxf(Mv, vi);
-          sm_o[i * ROWS + row] = vi;
-        }
-        const float top = warp_max(M);
-        L = warp_sum(L * fast_exp2(M - top));
-        Mv = warp_max(Mv);
-        for (int i = lane; i < n; i += 32) sm_o[i * ROWS + row] = fast_exp2(sm_o[i * ROWS + row] - Mv);
-        if (lane == 0) {
-          sm_f[row] = L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - top) : 1.f) / L;
-          lse_of(row, top, L);
+      const int i0 = tid - sl * tasks;
+      if (sl < S && i0 < tasks) fetch(i0, sl);
+      for (int x = tid; x < n * ROWS; x += kThreads) {
+        if (x % ROWS < nr) {
+          const float* v = slot(x / ROWS) + ROWS * D + x % ROWS;
+          st[x] = __ldcg(v), st[n * ROWS + x] = __ldcg(v + ROWS), st[2 * n * ROWS + x] = __ldcg(v + 2 * ROWS);
         }
       }
       __syncthreads();
-      for (int i = tid; i < nr * (D / 4); i += kThreads) {
-        const int row = i / (D / 4);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j0 = 0; j0 < n; j0 += kB) {
-          if (i != tid || j0 > 0) fetch(i, j0);
+#pragma unroll 1
+      for (int row = warp; row < nr; row += kWarps) {
+        float M = kNone, Mv = kNone, L = 0.f;
+        for (int i = lane; i < n; i += 32) {
+          M = fmaxf(M, st[i * ROWS + row]);
+          Mv = fmaxf(Mv, st[(n + i) * ROWS + row]);
+        }
+        M = warp_max(M);
+        Mv = warp_max(Mv);
+        for (int i = lane; i < n; i += 32) {
+          L += st[(2 * n + i) * ROWS + row] * fast_exp2(st[i * ROWS + row] - M);
+          st[(n + i) * ROWS + row] = fast_exp2(st[(n + i) * ROWS + row] - Mv);
+        }
+        L = warp_sum(L);
+        if (lane == 0) {
+          sm_f[row] = over_sum(M, Mv, L);
+          lse_of(row, M, L);
+        }
+      }
+      __syncthreads();
+      if (sl < S) {
+#pragma unroll 1
+        for (int i = i0; i < tasks; i += kThreads) {
+          const int row = i / (D / 4);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+          for (int j0 = sl; j0 < n; j0 += kB * S) {
+            if (i != i0 || j0 != sl) fetch(i, j0);
 #pragma unroll
-          for (int j = 0; j < kB; ++j) {
-            if (j0 + j < n) {
-              const float w = sm_o[(j0 + j) * ROWS + row];
-              x.x = fmaf(w, y[j].x, x.x);
-              x.y = fmaf(w, y[j].y, x.y);
-              x.z = fmaf(w, y[j].z, x.z);
-              x.w = fmaf(w, y[j].w, x.w);
+            for (int j = 0; j < kB; ++j) {
+              if (j0 + j * S < n) {
+                const float w = st[(n + j0 + j * S) * ROWS + row];
+                x.x = fmaf(w, y[j].x, x.x);
+                x.y = fmaf(w, y[j].y, x.y);
+                x.z = fmaf(w, y[j].z, x.z);
+                x.w = fmaf(w, y[j].w, x.w);
+              }
             }
           }
+          const float f = sm_f[row];
+          x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+          if (S > 1) sums[sl * tasks + i] = x;
+          else store4(sm_off[row] + (i % (D / 4)) * 4, x);
         }
-        const float f = sm_f[row];
-        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-        store4(sm_off[row] + (i % (D / 4)) * 4, x);
+      }
+      if (S > 1) {
+        __syncthreads();
+        if (tid < tasks) {
+          float4 x = sums[tid];
+          for (int j = 1; j < S; ++j) {
+            const float4 z = sums[j * tasks + tid];
+            x.x += z.x, x.y += z.y, x.z += z.z, x.w += z.w;
+          }
+          store4(sm_off[tid / (D / 4)] + (tid % (D / 4)) * 4, x);
+        }
       }
       if (tid == 0) *ctr = 0u;  // clean for the next call
     }
@@ -998,7 +1005,12 @@ cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   p.counter = static_cast<uint32_t*>(ws_body);
   p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
   Maps maps{};
-  if (C::FEED == kTma) {
+  // Heads side by side, so that the cache's rows, which hold all heads, are read whole at about the same
+  // time.  Only where few CTAs stay idle for it.
+  p.HG = p.Hkv <= P && (P % p.Hkv) * 16 <= P ? p.Hkv : 1;
+  p.nh = p.Hkv / p.HG;
+  p.PG = P / p.HG;
+  if (C::RING) {
     const uint64_t rows = (uint64_t)p.seqs * p.n_max, bytes = (uint64_t)p.Hkv * C::RB;
     if (!make_map(&maps.k, p.K, rows, bytes, std::min(C::RB, 128)) || !make_map(&maps.v, p.V, rows, bytes, std::min(C::RB, 128)))
       return cudaErrorInvalidValue;

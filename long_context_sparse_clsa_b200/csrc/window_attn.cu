@@ -38,9 +38,9 @@ template <typename F>
 auto dispatch(const clsa_window_args* a, int R, F&& f) {
   using namespace stream;
   const bool d128 = a->d == 128;
-  if (a->dtype == CLSA_F32) return d128 ? f(Cfg<kFp32, true, kLoads, 128, 1>{}) : f(Cfg<kFp32, true, kLoads, 64, 1>{});
-  if (row_tiles(R, false) == 1) return d128 ? f(Cfg<kBf16, false, kTma, 128, 1>{}) : f(Cfg<kBf16, false, kTma, 64, 1>{});
-  return d128 ? f(Cfg<kBf16, false, kTma, 128, 2>{}) : f(Cfg<kBf16, false, kTma, 64, 2>{});
+  if (a->dtype == CLSA_F32) return d128 ? f(Cfg<kFp32, true, false, 128, 1>{}) : f(Cfg<kFp32, true, false, 64, 1>{});
+  if (row_tiles(R, false) == 1) return d128 ? f(Cfg<kBf16, false, true, 128, 1>{}) : f(Cfg<kBf16, false, true, 64, 1>{});
+  return d128 ? f(Cfg<kBf16, false, true, 128, 2>{}) : f(Cfg<kBf16, false, true, 64, 2>{});
 }
 
 // Which form is faster, by a fit to both over T = 8 to 512, windows 256 to 8192, 1 to 4 sequences and five

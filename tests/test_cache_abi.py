@@ -139,3 +139,12 @@ def test_python_binding_refuses_tensors_off_the_gpu():
     with pytest.raises(ValueError):
         clsa.window_attn(torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16), torch.zeros(1, 9, 1, 64, dtype=torch.bfloat16),
                          torch.zeros(1, 9, 1, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), 4)
+
+
+def test_caches_behind_the_reach_of_their_loads_are_refused(lib):
+    """More than 2^31 - 4096 rows over all sequences."""
+    for n, want in ((1 << 29, UNSUPPORTED), ((1 << 29) - 1024, WORKSPACE)):
+        a = attn_args(B=4, cache=cache(B=4, n_max=n, Hkv=1))
+        assert lib.clsa_kv8_attn(ctypes.byref(a), P, 0, NULL) == want
+        a = window_args(B=4, n_max=n, Hkv=1)
+        assert lib.clsa_window_attn(ctypes.byref(a), P, 0, NULL) == want
