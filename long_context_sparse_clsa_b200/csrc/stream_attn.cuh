@@ -191,10 +191,10 @@ struct Cfg {
   // ring tiles of a warp: three (50.8 us over 128K tokens; 53.0 with four, 51.0 with two), or what there is room for
   static constexpr int ROOM = 192 * 1024 / (W * STAGE);
   static constexpr int NST = RING ? (ROOM < 3 ? ROOM : 3) : 1;
-  // dynamic shared memory: the ring; over it the warps' outputs, or the statistics of P contributors and
-  // their outputs' sums
+  // dynamic shared memory: the ring; over it the warps' outputs, or the weights of P parts and their outputs'
+  // sums
   static size_t smem(int P) {
-    return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 12 + W * 32 * 16}) + 1024;
+    return std::max({(size_t)W * NST * STAGE, (size_t)W * ROWS * D * 4, (size_t)P * ROWS * 4 + W * 32 * 16}) + 1024;
   }
 };
 
@@ -546,11 +546,14 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     } else {
       tok = token(t);
       tok_n = token(t + kWarps);
+      if constexpr (IDX) {                       // while the indices are on their way
+        if (warp < nw) load_q();
+      }
       sc = load_scale(tok);
       load_k(tok);
       load_v(tok);
     }
-    if constexpr (FP8) {
+    if constexpr (RING && FP8) {
       if (warp < nw) load_q();
     }
     if (tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
@@ -875,47 +878,63 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
         __stcg(x + 2 * ROWS, L);
       }
     }
+    // the merge: S threads per float4, each for every S-th part, kB loads in flight
+    constexpr int kB = 8;
+    const int S = tasks < kThreads ? min(kThreads / tasks, n) : 1, sl = S > 1 ? tid / tasks : 0, i0 = tid - sl * tasks;
     uint32_t* ctr = p.counter + (size_t)s * p.Hkv + g;
     __syncthreads();  // every thread's part is stored before the arrival, which releases them
     if (tid == 0) sm_last = atom_add_acq_rel_gpu(ctr, 1u) == (uint32_t)(n - 1);
     __syncthreads();
     if (sm_last) {      // the others' parts, released before their arrivals
-      // S threads per float4, each for every S-th part, kB loads in flight
-      constexpr int kB = 8;
-      const int S = tasks < kThreads ? min(kThreads / tasks, n) : 1, sl = S > 1 ? tid / tasks : 0;
-      float* const st = sm_o;                    // [3][n ROWS]: references, output references or weights, sums
-      float4* const sums = reinterpret_cast<float4*>(sm_o + (3 * n * ROWS + 3) / 4 * 4);
+      float* const wt = sm_o;                    // [n][ROWS]: the parts' weights
+      float4* const sums = reinterpret_cast<float4*>(sm_o + (n * ROWS + 3) / 4 * 4);
       float4 y[kB];
       auto fetch = [&](int i, int j0) {
 #pragma unroll
         for (int j = 0; j < kB; ++j) y[j] = __ldcg(reinterpret_cast<const float4*>(slot(min(j0 + j * S, n - 1))) + i);
       };
-      const int i0 = tid - sl * tasks;
       if (sl < S && i0 < tasks) fetch(i0, sl);
-      for (int x = tid; x < n * ROWS; x += kThreads) {
-        if (x % ROWS < nr) {
-          const float* v = slot(x / ROWS) + ROWS * D + x % ROWS;
-          st[x] = __ldcg(v), st[n * ROWS + x] = __ldcg(v + ROWS), st[2 * n * ROWS + x] = __ldcg(v + 2 * ROWS);
+      // a warp's rows (two at most), a lane per part
+      constexpr int RW = (ROWS + kWarps - 1) / kWarps;
+      float M[RW], Mv[RW], L[RW];
+#pragma unroll
+      for (int x = 0; x < RW; ++x) {
+        M[x] = Mv[x] = kNone;
+        L[x] = 0.f;
+      }
+#pragma unroll 1
+      for (int i = lane; i < n; i += 32) {
+        float mi[RW], vi[RW], li[RW];
+#pragma unroll
+        for (int x = 0; x < RW; ++x) {
+          const float* v = slot(i) + ROWS * D + min(warp + x * kWarps, nr - 1);
+          mi[x] = __ldcg(v), vi[x] = __ldcg(v + ROWS), li[x] = __ldcg(v + 2 * ROWS);
+        }
+#pragma unroll
+        for (int x = 0; x < RW; ++x) {
+          const float top = fmaxf(M[x], mi[x]);
+          L[x] = L[x] * fast_exp2(M[x] - top) + li[x] * fast_exp2(mi[x] - top);
+          M[x] = top;
+          Mv[x] = fmaxf(Mv[x], vi[x]);
+          if (warp + x * kWarps < nr) wt[i * ROWS + warp + x * kWarps] = vi[x];
         }
       }
-      __syncthreads();
-#pragma unroll 1
-      for (int row = warp; row < nr; row += kWarps) {
-        float M = kNone, Mv = kNone, L = 0.f;
-        for (int i = lane; i < n; i += 32) {
-          M = fmaxf(M, st[i * ROWS + row]);
-          Mv = fmaxf(Mv, st[(n + i) * ROWS + row]);
-        }
-        M = warp_max(M);
-        Mv = warp_max(Mv);
-        for (int i = lane; i < n; i += 32) {
-          L += st[(2 * n + i) * ROWS + row] * fast_exp2(st[i * ROWS + row] - M);
-          st[(n + i) * ROWS + row] = fast_exp2(st[(n + i) * ROWS + row] - Mv);
-        }
-        L = warp_sum(L);
-        if (lane == 0) {
-          sm_f[row] = over_sum(M, Mv, L);
-          lse_of(row, M, L);
+      float top[RW];
+#pragma unroll
+      for (int x = 0; x < RW; ++x) top[x] = warp_max(M[x]);
+#pragma unroll
+      for (int x = 0; x < RW; ++x) Mv[x] = warp_max(Mv[x]);
+#pragma unroll
+      for (int x = 0; x < RW; ++x) L[x] = warp_sum(L[x] * fast_exp2(M[x] - top[x]));
+#pragma unroll
+      for (int x = 0; x < RW; ++x) {
+        const int row = warp + x * kWarps;
+        if (row < nr) {
+          for (int i = lane; i < n; i += 32) wt[i * ROWS + row] = fast_exp2(wt[i * ROWS + row] - Mv[x]);
+          if (lane == 0) {
+            sm_f[row] = over_sum(top[x], Mv[x], L[x]);
+            lse_of(row, top[x], L[x]);
+          }
         }
       }
       __syncthreads();
@@ -930,7 +949,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
 #pragma unroll
             for (int j = 0; j < kB; ++j) {
               if (j0 + j * S < n) {
-                const float w = st[(n + j0 + j * S) * ROWS + row];
+                const float w = wt[(j0 + j * S) * ROWS + row];
                 x.x = fmaf(w, y[j].x, x.x);
                 x.y = fmaf(w, y[j].y, x.y);
                 x.z = fmaf(w, y[j].z, x.z);
