@@ -8,7 +8,7 @@
 //
 // Tokens.  The item's tokens form a line: the sinks (rounded up to 8), then the window's union
 // [lo, p_last].  It is cut into tiles of 128; a tile of window tokens is one TMA box, the tile
-// that holds the seam is 16 boxes of 8 rows.  Value rows of tokens that no row of the item
+// that holds the seam is boxes of 32 and 8 rows.  Value rows of tokens that no row of the item
 // sees are zeroed in shared memory, so their bytes do not matter (0 * NaN).
 //
 // Roles (one CTA per SM, persistent over items): one warp issues TMA loads into a ring of K and V
@@ -51,7 +51,7 @@ constexpr float kTau = 8.f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct Maps {
-  CUtensorMap q, k, v, k8, v8;  // k8, v8: boxes of 8 rows
+  CUtensorMap q, k, v, k8, v8, k32, v32;  // boxes of 128, 8 and 32 rows
 };
 
 struct WParams {
@@ -61,6 +61,7 @@ struct WParams {
   void* ws_header;
   int B, T, n_max, Hq, Hkv, G, TQ, nqt, window, sinks, items;
   float scale_log2;
+  bool wide;            // O is 32-byte aligned
 };
 
 template <int D>
@@ -155,6 +156,12 @@ __device__ __forceinline__ void st_32x32b_x8(uint32_t taddr, const uint32_t (&r)
                : "memory");
 }
 
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* x) {  // 32 bytes, 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
 // pairs of floats: two products or sums an instruction
 __device__ __forceinline__ uint64_t f32x2(float a, float b) {
   uint64_t r;
@@ -240,12 +247,15 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
           for (int a = 0; a < S::KA; ++a)
             tma_load_2d(dst + a * kAtom, v ? &maps.v : &maps.k, w.g * D + 64 * a, row0 + w.lo + pos - w.keepP, kv_full + slot);
         } else {
-          for (int r = 0; r < kTok; r += 8) {
+          for (int r = 0; r < kTok;) {
             const int q = pos + r;
             const int tok = q < w.keepP ? q : w.lo + q - w.keepP;
+            const bool big = r + 32 <= kTok && (q >= w.keepP || q + 32 <= w.keepP);
+            const CUtensorMap* map = big ? (v ? &maps.v32 : &maps.k32) : v ? &maps.v8 : &maps.k8;
 #pragma unroll
             for (int a = 0; a < S::KA; ++a)
-              tma_load_2d(dst + a * kAtom + r * 128, v ? &maps.v8 : &maps.k8, w.g * D + 64 * a, row0 + tok, kv_full + slot);
+              tma_load_2d(dst + a * kAtom + r * 128, map, w.g * D + 64 * a, row0 + tok, kv_full + slot);
+            r += big ? 32 : 8;
           }
         }
         ++n;
@@ -438,9 +448,15 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
         if (cw > 0 || w0 + kTok - 1 > pf || w0 <= pl - p.window) {
           const int cs = min(w.keepM, pr + 1) - j * kTok;
           const int cl = max(pr - p.window + 1 - w0, cw), ch = pr - w0;
+          // bits of the columns below x, 32 at a time: a test and a select per score
+          const auto below = [](int x) { return x <= 0 ? 0u : 0xffffffffu >> (32 - min(x, 32)); };
 #pragma unroll
-          for (int c = 0; c < kTok; ++c)
-            if (!(c < cs || (c >= cl && c <= ch))) v[c] = 0xff800000u;
+          for (int h = 0; h < kTok; h += 32) {
+            const uint32_t see = below(cs - h) | (below(ch + 1 - h) & ~below(cl - h));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!(see & (1u << c))) v[h + c] = 0xff800000u;
+          }
         }
         float x0 = kNone, x1 = kNone, x2 = kNone, x3 = kNone;
 #pragma unroll
@@ -512,15 +528,17 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
           uint32_t o[32];
           tc::ld_32x32b_x32(to + 32u * h, o);
           tc::ld_wait();
-          if (live) {
+          uint32_t x[16];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float* f = reinterpret_cast<const float*>(o) + 8 * c;
-              const bool none = l == 0.f;           // P = 0 everywhere: O is 0, not 0 * NaN
-              out[4 * h + c] = none ? make_uint4(0u, 0u, 0u, 0u)
-                                    : make_uint4(pack_bf16x2(f[0] * inv, f[1] * inv), pack_bf16x2(f[2] * inv, f[3] * inv),
-                                                 pack_bf16x2(f[4] * inv, f[5] * inv), pack_bf16x2(f[6] * inv, f[7] * inv));
-            }
+          for (int c = 0; c < 16; ++c)              // P = 0 everywhere: O is 0, not 0 * NaN
+            x[c] = l == 0.f ? 0u : pack_bf16x2(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+          // lanes write rows of their own: with 32 bytes a lane half the passes through L1 of 16 bytes
+          if (live && p.wide) {
+            st_global_v8(out + 4 * h, x);
+            st_global_v8(out + 4 * h + 2, x + 8);
+          } else if (live) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) out[4 * h + c] = make_uint4(x[4 * c], x[4 * c + 1], x[4 * c + 2], x[4 * c + 3]);
           }
         }
         tc::fence_before_sync();
@@ -595,13 +613,16 @@ cudaError_t launch_window_tc(const clsa_window_args* a, float scale, void* ws_he
   p.sinks = std::min(a->sinks, a->n_max);
   p.items = p.nqt * p.B * p.Hkv;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.wide = ((uintptr_t)a->O & 31) == 0;
   Maps maps;
   const uint64_t rows = (uint64_t)a->B * a->n_max, cols = (uint64_t)a->Hkv * a->d;
   if (!make_tmap_q(&maps.q, a->Q, a->d, a->Hq, (long long)a->B * a->T, p.G, p.TQ) ||
       !make_tmap_bf16_2d(&maps.k, a->K, rows, cols, cols * 2, kTok, 64) ||
       !make_tmap_bf16_2d(&maps.v, a->V, rows, cols, cols * 2, kTok, 64) ||
       !make_tmap_bf16_2d(&maps.k8, a->K, rows, cols, cols * 2, 8, 64) ||
-      !make_tmap_bf16_2d(&maps.v8, a->V, rows, cols, cols * 2, 8, 64))
+      !make_tmap_bf16_2d(&maps.v8, a->V, rows, cols, cols * 2, 8, 64) ||
+      !make_tmap_bf16_2d(&maps.k32, a->K, rows, cols, cols * 2, 32, 64) ||
+      !make_tmap_bf16_2d(&maps.v32, a->V, rows, cols, cols * 2, 32, 64))
     return cudaErrorInvalidValue;
   return a->d == 128 ? launch_d<128>(maps, p, s) : launch_d<64>(maps, p, s);
 }
