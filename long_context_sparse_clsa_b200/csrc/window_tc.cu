@@ -4,7 +4,10 @@
 // Rows.  The G query heads of a KV head share its keys, so a 128-row tile holds 128 / G tokens of
 // all G heads: a tile's rows then span few positions, and little of the window is scored for
 // rows that do not see it (G = 4, W = 1024: 1087 positions for 64 tokens; 64 tokens of one
-// head each would be 4 x 1087).  An item is two such tiles of one (sequence, KV head).
+// head each would be 4 x 1087).  An item is two such tiles of one (sequence, KV head); where the items
+// of the last round would leave half of the SMs idle, they are one tile each (a token tile of an item takes
+// a CTA about 2900 cycles with two row tiles, 2600 with one: T = 4096, W = 1024 83 -> 81 us, T = 512, W = 4096
+// 65 -> 59 us).
 //
 // Tokens.  The item's tokens form a line: the sinks (rounded up to 8), then the window's union
 // [lo, p_last].  It is cut into tiles of 128; a tile of window tokens is one TMA box, the tile
@@ -60,6 +63,7 @@ struct WParams {
   float* lse;           // [B][T][Hq] or null
   void* ws_header;
   int B, T, n_max, Hq, Hkv, G, TQ, nqt, window, sinks, items;
+  int whole;            // items from here on are one row tile each
   float scale_log2;
   bool wide;            // O is 32-byte aligned
 };
@@ -82,14 +86,20 @@ struct WItem {
 
 __device__ __forceinline__ WItem witem(const WParams& p, int i) {
   WItem w;
+  int rows = 2 * p.TQ, second = 0;
+  if (i >= p.whole) {
+    rows = p.TQ;
+    second = (i - p.whole) & 1;
+    i = p.whole + ((i - p.whole) >> 1);
+  }
   w.g = i % p.Hkv;
   i /= p.Hkv;
   w.b = i % p.B;
   const int qt = p.nqt - 1 - i / p.B;  // the latest rows (longest lines) first
-  w.t0 = qt * 2 * p.TQ;
+  w.t0 = qt * 2 * p.TQ + second * p.TQ;
   w.len = max(0, min(p.lens[w.b], p.n_max));
-  w.ntile = w.t0 + p.TQ < p.T ? 2 : 1;
-  const int first = w.len - p.T + w.t0, last = w.len - p.T + min(p.T, w.t0 + 2 * p.TQ) - 1;
+  w.ntile = rows > p.TQ && w.t0 + p.TQ < p.T ? 2 : 1;
+  const int first = w.len - p.T + w.t0, last = w.t0 < p.T ? w.len - p.T + min(p.T, w.t0 + rows) - 1 : -1;
   w.nkv = w.npos = 0;
   w.lo = w.keep = w.keepP = w.keepM = 0;
   if (last < 0) return w;
@@ -611,7 +621,12 @@ cudaError_t launch_window_tc(const clsa_window_args* a, float scale, void* ws_he
   p.nqt = (int)((a->T + 2LL * p.TQ - 1) / (2 * p.TQ));
   p.window = std::min(a->window, a->n_max);
   p.sinks = std::min(a->sinks, a->n_max);
-  p.items = p.nqt * p.B * p.Hkv;
+  p.items = p.whole = p.nqt * p.B * p.Hkv;
+  const int over = p.items % std::max(1, device_info().sm_count);
+  if (2 * over <= device_info().sm_count) {
+    p.whole = p.items - over;
+    p.items += over;
+  }
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wide = ((uintptr_t)a->O & 31) == 0;
   Maps maps;
