@@ -43,18 +43,24 @@ auto dispatch(const clsa_window_args* a, int R, F&& f) {
   return d128 ? f(Cfg<kBf16, false, true, 128, 2>{}) : f(Cfg<kBf16, false, true, 64, 2>{});
 }
 
-// Which form is faster, by a fit to both over T = 8 to 512, windows 256 to 8192, 1 to 4 sequences and five
-// head layouts (d = 128, us): the streaming form takes 10 + 1.6e-3 per (16 rows, 16 tokens), at
-// 75 to 105 TFLOP/s whatever the split; the tcgen05 form 9.5 + 1.55 per token tile and round of the
-// SMs, since few rows leave most SMs idle.  E.g. T = 24, window 8192: 39 and 98; T = 96: 133 and 110;
-// T = 48, window 256: 10 and 14; T = 512, window 1024: 125 and 25.
+// Which form is faster, by a fit to both over T = 2 to 512, windows 64 to 4096, 1 and 3 sequences and six
+// head layouts: of 352 shapes with more than 16 rows it picks one that is over 15 % slower 8 times, and on the
+// average loses 0.7 % (us, 148 SMs).  The streaming form: a start, 1.5e-3 per (16 rows, 16 tokens) at
+// d = 128, more where so many units share the SMs that a CTA goes through several.  The tcgen05
+// form: per round of the SMs 2, and 1.45 (items of one row tile: 1.35) per token tile, however few
+// SMs have an item.  E.g. 32 heads on 8, d = 128: T = 24, W = 4096 25 streaming and 51; T = 96, W = 1024
+// 30 and 18; 6 on 3, d = 64: T = 48, W = 4096 12 and 46; T = 512, W = 1024 28 and 16.
 bool use_tc(const clsa_window_args* a) {
   if (!window_tc_supported(a) || (long long)a->T * (a->Hq / a->Hkv) <= 16) return false;  // 16 rows: HBM is the bound
   const double G = a->Hq / a->Hkv, TQ = 128 / (a->Hq / a->Hkv), sms = std::max(1, device_info().sm_count);
   const double seen = std::min((double)a->n_max, (double)a->window + a->sinks);  // of one row
-  const double groups = std::ceil(a->T * G / 16) * a->B * a->Hkv, items = std::ceil(a->T / (2 * TQ)) * a->B * a->Hkv;
-  const double stream_us = 10 + 1.6e-3 * (a->d / 128.0) * groups * std::ceil((seen + 15) / 16) * (148 / sms);
-  const double tc_us = 9.5 + 1.55 * std::ceil(items / sms) * std::ceil(std::min((double)a->n_max, seen + 2 * TQ) / 128);
+  const double groups = std::ceil(a->T * G / 16) * a->B, units = groups * a->Hkv;
+  const double stream_us = 10 + 1.5e-3 * (0.5 + a->d / 256.0) * units * std::ceil((seen + 15) / 16) * (148 / sms) + (groups > 32 ? 6 : 0);
+  const double items = std::ceil(a->T / (2 * TQ)) * a->B * a->Hkv, over = std::fmod(items, sms);
+  const bool single = over > 0 && 2 * over <= sms;
+  const auto tiles = [&](double rows) { return std::ceil(std::min((double)a->n_max, seen + rows) / 128); };
+  const double rounds = std::floor(items / sms) + (over > 0 && !single ? 1 : 0);
+  const double tc_us = 4 + rounds * (2 + 1.45 * tiles(2 * TQ)) + (single ? 2 + 1.35 * tiles(TQ) : 0);
   return tc_us < stream_us;
 }
 

@@ -629,15 +629,17 @@ cudaError_t launch_window_tc(const clsa_window_args* a, float scale, void* ws_he
   }
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wide = ((uintptr_t)a->O & 31) == 0;
-  Maps maps;
+  Maps maps{};
   const uint64_t rows = (uint64_t)a->B * a->n_max, cols = (uint64_t)a->Hkv * a->d;
   if (!make_tmap_q(&maps.q, a->Q, a->d, a->Hq, (long long)a->B * a->T, p.G, p.TQ) ||
       !make_tmap_bf16_2d(&maps.k, a->K, rows, cols, cols * 2, kTok, 64) ||
-      !make_tmap_bf16_2d(&maps.v, a->V, rows, cols, cols * 2, kTok, 64) ||
-      !make_tmap_bf16_2d(&maps.k8, a->K, rows, cols, cols * 2, 8, 64) ||
-      !make_tmap_bf16_2d(&maps.v8, a->V, rows, cols, cols * 2, 8, 64) ||
-      !make_tmap_bf16_2d(&maps.k32, a->K, rows, cols, cols * 2, 32, 64) ||
-      !make_tmap_bf16_2d(&maps.v32, a->V, rows, cols, cols * 2, 32, 64))
+      !make_tmap_bf16_2d(&maps.v, a->V, rows, cols, cols * 2, kTok, 64))
+    return cudaErrorInvalidValue;
+  if (p.sinks > 0 &&  // the seam tile's boxes
+      (!make_tmap_bf16_2d(&maps.k8, a->K, rows, cols, cols * 2, 8, 64) ||
+       !make_tmap_bf16_2d(&maps.v8, a->V, rows, cols, cols * 2, 8, 64) ||
+       !make_tmap_bf16_2d(&maps.k32, a->K, rows, cols, cols * 2, 32, 64) ||
+       !make_tmap_bf16_2d(&maps.v32, a->V, rows, cols, cols * 2, 32, 64)))
     return cudaErrorInvalidValue;
   return a->d == 128 ? launch_d<128>(maps, p, s) : launch_d<64>(maps, p, s);
 }
