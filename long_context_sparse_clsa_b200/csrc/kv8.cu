@@ -20,7 +20,14 @@ namespace {
 
 constexpr int kThreadsW = 256;
 
-// 16 elements of a row, as floats
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t finite_abs_bits(float x) { return abs_bits(x) < 0x7f800000u ? abs_bits(x) : 0u; }
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  return (uint32_t)f32x2_to_e4m3x2(a, b) | ((uint32_t)f32x2_to_e4m3x2(c, d) << 16);
+}
+
+// 16 elements of a row: their largest |x| as a float's bits (at least 0x7f800000 where one is not finite),
+// the largest among the finite ones, and the codes of x * inv (inv a power of two)
 template <typename T> struct Load16;
 template <> struct Load16<__nv_bfloat16> {
   uint4 v[2];
@@ -29,12 +36,41 @@ template <> struct Load16<__nv_bfloat16> {
     v[1] = ld_stream_v4(p + 8);
   }
   __device__ __forceinline__ void zero() { v[0] = v[1] = make_uint4(0u, 0u, 0u, 0u); }
-  __device__ __forceinline__ float2 pair(int i) const {  // elements 2 i, 2 i + 1
+  __device__ __forceinline__ uint32_t word(int i) const {
     const uint4& q = v[i >> 2];
-    const uint32_t w = (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
-    float2 r;
-    unpack_bf16x2(w, r.x, r.y);
-    return r;
+    return (i & 3) == 0 ? q.x : (i & 3) == 1 ? q.y : (i & 3) == 2 ? q.z : q.w;
+  }
+  __device__ __forceinline__ uint32_t amax() const {  // two at a time
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(word(i) & 0x7fff7fffu));
+    return max(m << 16, m & 0xffff0000u);
+  }
+  __device__ __forceinline__ uint32_t amax_finite() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float a, b;
+      unpack_bf16x2(word(i), a, b);
+      m = max(m, max(finite_abs_bits(a), finite_abs_bits(b)));
+    }
+    return m;
+  }
+  // the products are exact in bf16 but below 2^-126, where the code is 0 anyway
+  __device__ __forceinline__ uint4 codes(float inv) const {
+    const uint32_t i2 = pack_bf16x2(inv, inv);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t x, y;
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(x) : "r"(word(2 * e)), "r"(i2));
+      asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(word(2 * e + 1)), "r"(i2));
+      float a, b, c, d;
+      unpack_bf16x2(x, a, b);
+      unpack_bf16x2(y, c, d);
+      w[e] = e4m3x4(a, b, c, d);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 template <> struct Load16<float> {
@@ -47,16 +83,41 @@ template <> struct Load16<float> {
 #pragma unroll
     for (int i = 0; i < 4; ++i) v[i] = make_uint4(0u, 0u, 0u, 0u);
   }
-  __device__ __forceinline__ float2 pair(int i) const {
-    const uint4& q = v[i >> 1];
-    return (i & 1) ? make_float2(__uint_as_float(q.z), __uint_as_float(q.w))
-                   : make_float2(__uint_as_float(q.x), __uint_as_float(q.y));
+  __device__ __forceinline__ uint32_t amax() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m = max(m, max(v[i].x & 0x7fffffffu, v[i].y & 0x7fffffffu));
+      m = max(m, max(v[i].z & 0x7fffffffu, v[i].w & 0x7fffffffu));
+    }
+    return m;
+  }
+  __device__ __forceinline__ uint32_t amax_finite() const {
+    uint32_t m = 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m = max(m, max(finite_abs_bits(__uint_as_float(v[i].x)), finite_abs_bits(__uint_as_float(v[i].y))));
+      m = max(m, max(finite_abs_bits(__uint_as_float(v[i].z)), finite_abs_bits(__uint_as_float(v[i].w))));
+    }
+    return m;
+  }
+  __device__ __forceinline__ uint4 codes(float inv) const {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = e4m3x4(__uint_as_float(v[e].x) * inv, __uint_as_float(v[e].y) * inv, __uint_as_float(v[e].z) * inv,
+                    __uint_as_float(v[e].w) * inv);
+    return make_uint4(w[0], w[1], w[2], w[3]);
   }
 };
 
-__device__ __forceinline__ uint32_t finite_abs_bits(float x) {
-  const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
-  return u < 0x7f800000u ? u : 0u;
+// the largest of the threads' values; `s_max` is free again behind the caller's next barrier
+__device__ __forceinline__ uint32_t cta_max(uint32_t mx, uint32_t* s_max) {
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
+  __syncthreads();
+  const uint4 a = *reinterpret_cast<const uint4*>(s_max), b = *reinterpret_cast<const uint4*>(s_max + 4);
+  return max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
 }
 
 struct WriteParams {
@@ -69,17 +130,20 @@ struct WriteParams {
   float* ks;               // [B][nblk][Hkv]
   float* vs;
   void* ws_header;
-  int B, T, n_max, Hkv, d, block, nblk, jmax;
+  int B, T, n_max, Hkv, d, block, bshift, nblk, jmax;
 };
 
 // One CTA per (sequence, block of tokens that the new rows touch, head, K or V): the block's
 // new rows stay in registers between their maximum and their codes, so they are read once.
 // A thread holds NU units of 16 elements.  No two CTAs share a block's scale or codes.
-// 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64: 36.9 us.
+// Elements are handled two at a time (packed maximum and product), and those that are not finite only where
+// the maximum shows one: 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64, take 28.0 us; 37.0 one
+// element at a time, with the integer pipe the bound.
 template <typename T, int NU>
 __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams p) {
   pdl_enter();
-  __shared__ uint32_t s_max[kThreadsW / 32];
+  static_assert(kThreadsW == 256, "eight warps");
+  __shared__ __align__(16) uint32_t s_max[2][kThreadsW / 32];
   unsigned u = blockIdx.x;  // (which, head, j, b), which fastest
   const bool isv = u & 1u;
   u >>= 1;
@@ -95,8 +159,8 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
       record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)p0);
     return;
   }
-  const int blk = p0 / p.block + j;
-  if (j > (p0 + cnt - 1) / p.block - p0 / p.block) return;  // behind the last block touched
+  const int blk = (p0 >> p.bshift) + j;
+  if (blk > (p0 + cnt - 1) >> p.bshift) return;  // behind the last block touched
   const int first = blk * p.block;         // the block's first token
   const int lo = max(first, p0);           // new rows of this block: tokens [lo, hi)
   const int hi = min(first + p.block, p0 + cnt);
@@ -118,33 +182,21 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
     else x[i].zero();
   }
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
+  for (int i = 0; i < NU; ++i) mx = max(mx, x[i].amax());
+  mx = cta_max(mx, s_max[0]);              // also: every thread has read the old scale
+  if (mx >= 0x7f800000u) {                 // something is not finite: the largest of the rest
+    mx = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float2 f = x[i].pair(e);
-      mx = max(mx, max(finite_abs_bits(f.x), finite_abs_bits(f.y)));
-    }
+    for (int i = 0; i < NU; ++i) mx = max(mx, x[i].amax_finite());
+    mx = cta_max(mx, s_max[1]);
   }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
-  __syncthreads();  // also: every thread has read the old scale
-#pragma unroll
-  for (int w = 0; w < kThreadsW / 32; ++w) mx = max(mx, s_max[w]);
   float s = exp2_int(kv8_scale_exp(mx));
   if (kept) s = fmaxf(s, s_old);
   const float inv = 1.f / s;               // exact: s is a power of two
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
     const int v = threadIdx.x + i * kThreadsW;
-    if (v < units) {
-      uint32_t w[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = x[i].pair(2 * e), g = x[i].pair(2 * e + 1);
-        w[e] = (uint32_t)f32x2_to_e4m3x2(f.x * inv, f.y * inv) | ((uint32_t)f32x2_to_e4m3x2(g.x * inv, g.y * inv) << 16);
-      }
-      *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
+    if (v < units) *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = x[i].codes(inv);
   }
   if (threadIdx.x == 0 && !(kept && s == s_old)) *sc = s;
   if (kept && s > s_old) {                 // the earlier rows move to the larger scale
@@ -157,7 +209,7 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float2 f = e4m3x2_to_f32x2((uint16_t)w[e]), g = e4m3x2_to_f32x2((uint16_t)(w[e] >> 16));
-        w[e] = (uint32_t)f32x2_to_e4m3x2(f.x * r, f.y * r) | ((uint32_t)f32x2_to_e4m3x2(g.x * r, g.y * r) << 16);
+        w[e] = e4m3x4(f.x * r, f.y * r, g.x * r, g.y * r);
       }
       *at = q;
     }
@@ -287,6 +339,7 @@ cudaError_t launch_kv8_write(const clsa_kv8_cache* c, const void* K, const void*
   p.d = c->d;
   p.block = c->block;
   p.nblk = (c->n_max + c->block - 1) / c->block;
+  p.bshift = log2_of(c->block);
   p.jmax = (int)write_jmax(T, c->block);
   const cudaError_t e = dt == CLSA_BF16 ? launch_write<__nv_bfloat16>(p, s) : launch_write<float>(p, s);
   launches_add(1, s);
