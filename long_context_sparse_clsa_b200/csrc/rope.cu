@@ -5,7 +5,7 @@
 //   (x1, x2) -> m (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
 //
 // The kernel moves every element in and out once: HBM is the bound (671 MB for 32768
-// tokens of 32 + 8 heads, d = 128, bf16).  The angles need care and cost little: pos f_i
+// tokens of 32 + 8 heads, d = 128, bf16: 101.8 us, 6.6 TB/s).  The angles need care and cost little: pos f_i
 // reaches 10^5 and more radians, so f_i / 2 pi comes as fp64 from the host, the product and
 // its reduction to half a turn are fp64, and sine and cosine of the reduced angle fp32.
 // One table per token serves all its heads (rot/2 entries in shared memory); a CTA issues
@@ -70,7 +70,7 @@ template <> struct Vec16<float> {
 // A thread owns one vector (c, threadIdx.x) of the heads of one token (threadIdx.z): its cosines and
 // sines stay in registers while it walks the heads threadIdx.y, + blockDim.y, ..., kHeads of
 // them in flight.  (With a flat index and a table look-up per vector the kernel was bound by its
-// own instructions: 127 us for 671 MB, against the figure above.)
+// own instructions: 127 us for the 671 MB.)
 template <typename T, bool HALF>
 __global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams p) {
   pdl_enter();
