@@ -623,7 +623,7 @@ def kv8_attn(Q, cache: Kv8Cache, count, idx=None, scale: float = 0.0, ws: Option
     a = _kv8_attn_args(dev, Q, cache, count, idx, scale, O, lse)
     ref = ctypes.byref(a)
     if ws is None:
-        ws = Workspace(_need(lib.clsa_kv8_attn_workspace_size(ref), "clsa_kv8_attn_workspace_size"), Q.device)
+        ws = Workspace(lib.clsa_kv8_attn_workspace_size(ref), Q.device)  # 0: the call says why
     _check(lib.clsa_kv8_attn(ref, _ws(ws, dev), ws.nbytes, stream), "clsa_kv8_attn")
     return (O[0], lse[0] if lse is not None else None) if squeeze else (O, lse)
 
@@ -658,7 +658,7 @@ def window_attn(Q, K, V, seq_lens, window: int, sinks: int = 0, scale: float = 0
     a = _window_args(dev, Q, K, V, seq_lens, window, sinks, scale, O, lse)
     ref = ctypes.byref(a)
     if ws is None:
-        ws = Workspace(_need(lib.clsa_window_attn_workspace_size(ref), "clsa_window_attn_workspace_size"), Q.device)
+        ws = Workspace(lib.clsa_window_attn_workspace_size(ref), Q.device)  # 0: the call says why
     _check(lib.clsa_window_attn(ref, _ws(ws, dev), ws.nbytes, stream), "clsa_window_attn")
     return O, lse
 

@@ -14,7 +14,6 @@
 // the second ("half"), or 16 bytes ("interleaved"); so outputs may overwrite their inputs.
 #include <algorithm>
 #include <cmath>
-#include <cstring>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -156,7 +155,7 @@ __global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams 
   }
 }
 
-// turns per token of each pair: f_i / 2 pi
+// turns per token of each pair: f_i / 2 pi (under 1 us of the host for 64 pairs)
 void rope_turns(const clsa_rope_args* a, double* turns) {
   const double two_pi = 6.283185307179586476925286766559;
   double theta = a->theta;
@@ -177,24 +176,7 @@ void rope_turns(const clsa_rope_args* a, double* turns) {
 
 cudaError_t launch_rope(const clsa_rope_args* a, cudaStream_t s) {
   RopeParams p{};
-  // the table of the last parameters this host thread used (64 powers cost more than a launch)
-  static thread_local struct {
-    bool set = false;
-    int rot, scaling, orig_len;
-    double v[4];
-    double turns[kMaxPairs];
-  } memo;
-  const double v[4] = {a->theta, a->factor, a->beta_fast, a->beta_slow};
-  if (!memo.set || memo.rot != a->rot || memo.scaling != a->scaling || memo.orig_len != a->orig_len ||
-      std::memcmp(memo.v, v, sizeof v) != 0) {
-    rope_turns(a, memo.turns);
-    memo.rot = a->rot;
-    memo.scaling = a->scaling;
-    memo.orig_len = a->orig_len;
-    std::memcpy(memo.v, v, sizeof v);
-    memo.set = true;
-  }
-  std::memcpy(p.turns, memo.turns, sizeof p.turns);
+  rope_turns(a, p.turns);
   p.q = a->q;
   p.k = a->k;
   p.pos = a->pos;
