@@ -3,10 +3,17 @@
 //   O[r] = sum_j p_rj v_j / sum_j p_rj,   p_rj = exp(q_r . k_j * scale),  j over the tokens r sees.
 //
 // What bounds it is moving K and V: with G query heads per KV head a byte of the cache feeds 2 G
-// multiplies.  So every warp is a stream of its own, with no barrier in its loop: it takes
-// tiles of 16 tokens, brings K and V to the registers that feed the tensor core (mma.sync m16n8k16; a 128-row tcgen05 tile would be empty for G = 4), keeps a running
-// maximum, sum and output for its rows, and issues the next tile's loads as soon as the
-// registers are free.  Nothing of the cache passes through shared memory.
+// multiplies.  So every warp is a stream of its own, with no barrier in its loop: it takes tiles of
+// 16 tokens, multiplies them on the tensor core (mma.sync m16n8k16; a 128-row tcgen05 tile would be
+// empty for G = 4) and keeps a running maximum, sum and output for its rows.  Consecutive tokens
+// come by TMA through a ring of the warp's own in shared memory (three tiles ahead: 147 KB in flight
+// on an SM at d = 128); an index list's, and fp32 ones, by plain loads into the registers that
+// feed the tensor core, one tile ahead (an index list through a ring of asynchronous copies
+// took 17.4 us for 24 layers and 2048 tokens, by loads 16.3).
+// Measured (32 heads on 8, d = 128): 131072 tokens of the 8-bit cache 49.5 us, 5.4 TB/s, of which the
+// loop takes 41, at the rate of a plain copy, and 8 go to the launch, the plan and the merge; 16
+// sequences of 16K to 128K tokens 277 us, 6.1 TB/s; 1028 bf16 tokens of 16 sequences 13.2 us; 24 layers
+// over 2048 selected tokens 15.5 us, a chain of latencies (plan 1.5, indices and first rows 3, loop 6, merge 4).
 //
 // Fragments.  Both products are computed transposed, so that 16 is the token axis and 8 the row
 // axis (R <= 8 rows waste nothing):
@@ -30,9 +37,9 @@
 // halves it is 2^7 larger still (halves end at 2^16), so that the halves' smallest step, 2^-24,
 // is 2^-31 of the largest.
 //
-// Work split.  A unit is a (sequence, row group, KV head).  Few units of like length get whole CTAs
-// each; else all units' tiles form one line that the CTAs share equally, so ragged lengths
-// balance.  A unit that several CTAs share is merged by the one that arrives last, in CTA
+// Work split.  A unit is a (sequence, row group, KV head); the heads of the same tokens go to CTAs side by
+// side.  Few units of like length get whole CTAs each; else all units' tiles form one line that the
+// CTAs share equally, so ragged lengths balance.  A unit that several CTAs share is merged by the one that arrives last, in CTA
 // order (the result does not depend on who that is).
 #pragma once
 

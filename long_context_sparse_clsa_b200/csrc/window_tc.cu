@@ -26,6 +26,11 @@
 // then O is rescaled in TMEM.  A row's softmax needs no exchange: its 128 scores are one lane.
 // Bound: per token tile and row tile 2 x 128 x 128 x d multiplies and 128 x 128 exponentials, which at
 // d = 128 take the tensor cores and the special-function units about 1024 cycles each.
+// Measured (32 heads on 8, d = 128): T = 16381, W = 4096 840 us, 1.15 PFLOP/s of visible products; T = 4096,
+// W = 1024 75 us, 0.92 PFLOP/s.  A step of both row tiles takes about 2950 cycles: 1450 for a tile's
+// exponentials and P, 400 for its scores and maximum, then 920 until P V and the next S are through
+// (768 of them products); the two tiles' chains overlap, but neither pipe fills (tensor cores active 49 %
+// at W = 1024).  A change of item costs about 5000 cycles more, partly filled tiles the rest.
 //
 // Every wait is bounded; one that runs out records CLSA_ERR_TIMEOUT and the CTA drains its
 // loads and returns.
