@@ -272,8 +272,9 @@ CLSA_API clsa_status clsa_prefill_attention(const clsa_prefill_args* a, int mode
  * device int32, any value).  Nq and Nk are multiples of n_pos: Q [L][B][Hq][d] of L layers
  * with one position per sequence is Nq = L B, n_pos = B.  q or k may be NULL (its row count
  * 0); q_out may equal q and k_out may equal k, else no buffer overlaps another.
- * d in {64, 128}; rot a multiple of 16, 16 <= rot <= d.  Angles are reduced in fp64, sines and
- * products are fp32, one rounding to dtype.  mscale <= 0 selects 1.  Needs no workspace. */
+ * d in {64, 128}; rot a multiple of 16, 16 <= rot <= d.  Angles are reduced to one turn in
+ * 64-bit fixed point, sines and products are fp32, one rounding to dtype.  Frequencies of 2^52 turns
+ * a token and more are refused (CLSA_ERR_INVALID_ARG).  mscale <= 0 selects 1.  Needs no workspace. */
 typedef enum clsa_rope_layout { CLSA_ROPE_HALF = 0, CLSA_ROPE_INTERLEAVED = 1 } clsa_rope_layout;
 typedef enum clsa_rope_scaling {
   CLSA_ROPE_PLAIN = 0,

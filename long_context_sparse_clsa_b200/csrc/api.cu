@@ -367,7 +367,8 @@ clsa_status clsa_rope(const clsa_rope_args* a, void* stream) {
   for (const void* p : {a->q, a->k, (const void*)a->q_out, (const void*)a->k_out})
     if (p && !aligned16(p)) return CLSA_ERR_INVALID_ARG;
   if (!aligned4(a->pos)) return CLSA_ERR_INVALID_ARG;
-  return from_cuda(launch_rope(a, static_cast<cudaStream_t>(stream)));
+  const cudaError_t e = launch_rope(a, static_cast<cudaStream_t>(stream));
+  return e == cudaErrorInvalidValue ? CLSA_ERR_INVALID_ARG : from_cuda(e);  // frequencies out of range
 }
 
 size_t clsa_kv8_workspace_size(void) { return kWsHeader; }

@@ -5,15 +5,19 @@
 //   (x1, x2) -> m (x1 cos a - x2 sin a, x2 cos a + x1 sin a)
 //
 // The kernel moves every element in and out once: HBM is the bound (671 MB for 32768
-// tokens of 32 + 8 heads, d = 128, bf16: 101.8 us, 6.6 TB/s).  The angles need care and cost little: pos f_i
-// reaches 10^5 and more radians, so f_i / 2 pi comes as fp64 from the host, the product and
-// its reduction to half a turn are fp64, and sine and cosine of the reduced angle fp32.
-// One table per token serves all its heads (rot/2 entries in shared memory); a CTA issues
-// its first loads before it computes the table, so the fp64 work hides behind them.
+// tokens of 32 + 8 heads, d = 128, bf16: 101.3 us, 6.6 TB/s; 537 MB for 131072 tokens of 8 heads: 87 us, 6.2 TB/s).  The
+// angles need care: pos f_i reaches 10^5 and more radians.  f_i / 2 pi comes from the host as a 64-bit
+// fraction of a turn, so that its product with pos, cut to 64 bits, is the angle reduced to one
+// turn (off by pos 2^-65 turns); its upper 32 bits go to fp32 and into sine and cosine.  One table per
+// token serves all its heads (rot/2 entries in shared memory); a CTA issues its first loads before it
+// computes the table.  With few heads a token the table is the larger part: with fp64 products, and the
+// fractions read from the parameters by index (32 addresses a warp, one after the other), the 537 MB
+// took 134 us.
 // A unit of work is what one thread can turn alone: 16 bytes of the first half and 16 of
 // the second ("half"), or 16 bytes ("interleaved"); so outputs may overwrite their inputs.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -25,7 +29,7 @@ namespace {
 constexpr int kMaxPairs = 64;      // d <= 128
 constexpr int kMaxTokRope = 16;    // tokens per CTA
 constexpr int kMaxThreadsRope = 256;
-constexpr int kHeads = 5;               // heads of a thread in flight
+constexpr int kMaxHeads = 5;       // heads of a thread in flight
 
 struct RopeParams {
   const void* q;
@@ -37,7 +41,7 @@ struct RopeParams {
   int Hq, Hk, d, rot;
   int tpc;             // tokens per CTA
   float mscale, sign;  // sign: -1 for the transpose
-  double turns[kMaxPairs];
+  uint64_t turns[kMaxPairs];  // of a token, in 2^-64 turns
 };
 
 template <typename T> struct Vec16;
@@ -68,10 +72,10 @@ template <> struct Vec16<float> {
 
 // A thread owns one vector (c, threadIdx.x) of the heads of one token (threadIdx.z): its cosines and
 // sines stay in registers while it walks the heads threadIdx.y, + blockDim.y, ..., kHeads of
-// them in flight.  (With a flat index and a table look-up per vector the kernel was bound by its
+// them in flight (2, 4 or 5: what a thread does not need costs registers and instructions).  (With a flat index and a table look-up per vector the kernel was bound by its
 // own instructions: 127 us for the 671 MB.)
-template <typename T, bool HALF>
-__global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams p) {
+template <typename T, bool HALF, int kHeads>
+__global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const __grid_constant__ RopeParams p) {
   pdl_enter();
   constexpr int N = Vec16<T>::N, NC = HALF ? N : N / 2;  // elements, pairs of a vector
   __shared__ __align__(16) float2 tab[kMaxTokRope][kMaxPairs];
@@ -106,10 +110,12 @@ __global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams 
   const int ntok = min(p.tpc, p.n_pos - (int)blockIdx.x * p.tpc);
   for (int i = me; i < ntok * half; i += nt) {
     const int t = i / half, f = i - t * half;
-    double x = (double)p.pos[blockIdx.x * p.tpc + t] * p.turns[f];
-    x -= rint(x);                              // turns, in [-1/2, 1/2]
+    uint64_t turns;                            // a load by address: the lanes' entries lie side by side
+    asm("ld.u64 %0, [%1];" : "=l"(turns) : "l"(p.turns + f));
+    const uint64_t x = (uint64_t)(int64_t)p.pos[blockIdx.x * p.tpc + t] * turns;
+    const int h = (int)((x + 0x80000000u) >> 32);  // in 2^-32 turns, from -1/2 to 1/2
     float sn, cs;
-    sincospif((float)(2.0 * x), &sn, &cs);
+    sincospif((float)h * 0x1p-31f, &sn, &cs);
     tab[t][f] = make_float2(cs * p.mscale, sn * p.mscale * p.sign);
   }
   __syncthreads();
@@ -155,8 +161,9 @@ __global__ void __launch_bounds__(kMaxThreadsRope) rope_kernel(const RopeParams 
   }
 }
 
-// turns per token of each pair: f_i / 2 pi (under 1 us of the host for 64 pairs)
-void rope_turns(const clsa_rope_args* a, double* turns) {
+// turns per token of each pair, f_i / 2 pi, without the whole ones (under 1 us of the host for 64 pairs);
+// false: a frequency is so large that a double holds no part of a turn
+bool rope_turns(const clsa_rope_args* a, uint64_t* turns) {
   const double two_pi = 6.283185307179586476925286766559;
   double theta = a->theta;
   if (a->scaling == CLSA_ROPE_BASE) theta *= std::pow(a->factor, (double)a->rot / (a->rot - 2));
@@ -168,15 +175,18 @@ void rope_turns(const clsa_rope_args* a, double* turns) {
       const double g = std::min(1.0, std::max(0.0, (r - a->beta_slow) / (a->beta_fast - a->beta_slow)));
       f = g * f + (1.0 - g) * f / a->factor;
     }
-    turns[i] = f / two_pi;
+    const double x = f / two_pi, part = x - std::floor(x);
+    if (!(x < 0x1p52)) return false;
+    turns[i] = (uint64_t)std::ldexp(part, 63) << 1;  // part < 1 of 53 bits: no bit is lost above 2^-63
   }
+  return true;
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const clsa_rope_args* a, cudaStream_t s) {
   RopeParams p{};
-  rope_turns(a, p.turns);
+  if (!rope_turns(a, p.turns)) return cudaErrorInvalidValue;
   p.q = a->q;
   p.k = a->k;
   p.pos = a->pos;
@@ -195,26 +205,30 @@ cudaError_t launch_rope(const clsa_rope_args* a, cudaStream_t s) {
   const bool half = a->layout == CLSA_ROPE_HALF;
   const int uph = (half ? a->rot / 2 : a->rot) / n + (a->d - a->rot) / n;  // vectors (or pairs of them) of a head: 4 to 32
   const int nh = p.jq * p.Hq + p.jk * p.Hk;
-  // Many positions: up to kHeads heads a thread, in whole warps (100.8 us for 32768 x 40 heads; 105.5
-  // with 4 heads a thread, 80 threads a CTA; 150 with one).  Few: more threads, two heads each
+  // Many positions: up to kMaxHeads heads a thread, CTAs of 64 threads (101.3 us for 32768 x 40 heads; 105 with
+  // two heads a thread; 87 for 131072 x 8 heads, 90 with 128 threads).  Few: more threads, two heads each
   // (2.3 us for 16 x 40 heads; 3.1 with five).
   const bool many = a->n_pos >= 4 * device_info().sm_count;
-  int fit = 1;
-  while (fit < 32 && uph * fit % 32 != 0) fit *= 2;  // heads side by side that fill whole warps
-  int hy = many ? (nh + kHeads - 1) / kHeads : (nh + 1) / 2;
-  if (many) hy = (hy + fit - 1) / fit * fit;
-  hy = std::max(1, std::min({hy, nh, kMaxThreadsRope / uph}));
+  int hy = 1;
+  if (!many) hy = (nh + 1) / 2;
+  else while (hy * kMaxHeads < nh) hy *= 2;
+  hy = std::max(1, std::min(hy, kMaxThreadsRope / uph));
+  const int heads = (nh + hy - 1) / hy;           // of a thread
   const int spread = std::max(1, a->n_pos / (4 * std::max(1, device_info().sm_count)));
-  p.tpc = std::max(1, std::min({kMaxTokRope, 128 / (uph * hy), spread}));
+  p.tpc = std::max(1, std::min({kMaxTokRope, 64 / (uph * hy), spread}));
   const dim3 threads(uph, hy, p.tpc);
   const dim3 grid((a->n_pos + p.tpc - 1) / p.tpc);
-  cudaError_t e;
-  if (a->dtype == CLSA_BF16)
-    e = half ? launch_pdl(rope_kernel<__nv_bfloat16, true>, grid, threads, 0, s, p)
-             : launch_pdl(rope_kernel<__nv_bfloat16, false>, grid, threads, 0, s, p);
-  else
-    e = half ? launch_pdl(rope_kernel<float, true>, grid, threads, 0, s, p)
-             : launch_pdl(rope_kernel<float, false>, grid, threads, 0, s, p);
+  const auto go = [&](auto kh) {
+    constexpr int KH = decltype(kh)::value;
+    if (a->dtype == CLSA_BF16)
+      return half ? launch_pdl(rope_kernel<__nv_bfloat16, true, KH>, grid, threads, 0, s, p)
+                  : launch_pdl(rope_kernel<__nv_bfloat16, false, KH>, grid, threads, 0, s, p);
+    return half ? launch_pdl(rope_kernel<float, true, KH>, grid, threads, 0, s, p)
+                : launch_pdl(rope_kernel<float, false, KH>, grid, threads, 0, s, p);
+  };
+  const cudaError_t e = heads <= 2   ? go(std::integral_constant<int, 2>{})
+                        : heads == 4 ? go(std::integral_constant<int, 4>{})
+                                     : go(std::integral_constant<int, 5>{});
   launches_add(1, s);
   return e;
 }

@@ -148,3 +148,10 @@ def test_caches_behind_the_reach_of_their_loads_are_refused(lib):
         assert lib.clsa_kv8_attn(ctypes.byref(a), P, 0, NULL) == want
         a = window_args(B=4, n_max=n, Hkv=1)
         assert lib.clsa_window_attn(ctypes.byref(a), P, 0, NULL) == want
+
+
+def test_rope_refuses_frequencies_out_of_range(lib):
+    """Frequencies that leave a double's range, or that no longer have a part of a turn."""
+    for kw in ({"scaling": 1, "factor": 1e-310}, {"scaling": 1, "factor": 1e-17}, {"scaling": 2, "factor": 1e-300},
+               {"scaling": 3, "factor": 1e-300, "orig_len": 1}):
+        assert lib.clsa_rope(ctypes.byref(rope_args(**kw)), NULL) == INVALID, kw
