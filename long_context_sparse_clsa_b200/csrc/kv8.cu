@@ -10,9 +10,11 @@
 //
 // Both kernels move bytes: HBM (long runs) or launch latency (a decode step) is the bound.
 #include <algorithm>
+#include <cmath>
 
 #include "fp8.cuh"
 #include "kernels.h"
+#include "vec32.cuh"
 
 namespace clsa {
 
@@ -31,7 +33,7 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 template <typename T> struct Load16;
 template <> struct Load16<__nv_bfloat16> {
   uint4 v[2];
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+  __device__ __forceinline__ void load(const __nv_bfloat16* p, bool) {  // 32-byte loads took the same time or more
     v[0] = ld_stream_v4(p);
     v[1] = ld_stream_v4(p + 8);
   }
@@ -75,9 +77,9 @@ template <> struct Load16<__nv_bfloat16> {
 };
 template <> struct Load16<float> {
   uint4 v[4];
-  __device__ __forceinline__ void load(const float* p) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ld_stream_v4(p + 4 * i);
+  __device__ __forceinline__ void load(const float* p, bool wide) {
+    ld_stream_32(p, v[0], v[1], wide);
+    ld_stream_32(p + 8, v[2], v[3], wide);
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
@@ -111,13 +113,21 @@ template <> struct Load16<float> {
   }
 };
 
-// the largest of the threads' values; `s_max` is free again behind the caller's next barrier
-__device__ __forceinline__ uint32_t cta_max(uint32_t mx, uint32_t* s_max) {
+// the largest of the values of this thread's group of 2^GS threads, and of all groups; `s_max` is free
+// again behind the caller's next barrier
+template <int GS>
+__device__ __forceinline__ uint32_t group_max(uint32_t mx, uint32_t* s_max, uint32_t& all) {
   mx = __reduce_max_sync(0xffffffffu, mx);
   if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = mx;
   __syncthreads();
-  const uint4 a = *reinterpret_cast<const uint4*>(s_max), b = *reinterpret_cast<const uint4*>(s_max + 4);
-  return max(max(max(a.x, a.y), max(a.z, a.w)), max(max(b.x, b.y), max(b.z, b.w)));
+  all = 0u;
+  const int mine = threadIdx.x >> GS;
+#pragma unroll
+  for (int w = 0; w < kThreadsW / 32; ++w) {
+    all = max(all, s_max[w]);
+    if (GS == 8 || w >> (GS - 5) == mine) mx = max(mx, s_max[w]);
+  }
+  return mx;
 }
 
 struct WriteParams {
@@ -131,31 +141,39 @@ struct WriteParams {
   float* vs;
   void* ws_header;
   int B, T, n_max, Hkv, d, block, bshift, nblk, jmax;
+  int hgroups;             // groups of 256 >> GS heads
+  bool wide;               // K and V are 32-byte aligned
 };
 
-// One CTA per (sequence, block of tokens that the new rows touch, head, K or V): the block's
-// new rows stay in registers between their maximum and their codes, so they are read once.
-// A thread holds NU units of 16 elements.  No two CTAs share a block's scale or codes.
+// One CTA per (sequence, block of tokens that the new rows touch, head, K or V), or for as many heads as
+// its threads hold blocks of (2^GS threads a head): the block's new rows stay in registers between
+// their maximum and their codes, so they are read once.  A thread holds NU units of 16 elements.  No two CTAs share a
+// block's scale or codes.
 // Elements are handled two at a time (packed maximum and product), and those that are not finite only where
-// the maximum shows one: 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64, take 28.0 us; 37.0 one
-// element at a time, with the integer pipe the bound.
-template <typename T, int NU>
-__global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams p) {
+// the maximum shows one: 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64, take 27.5 us; 37.0 one
+// element at a time, with the integer pipe the bound.  2 x 16384 rows: bf16 30.3 us, 6.6 TB/s, fp32 49.4 (56.6
+// with loads of 16 bytes, of which a lane takes every fourth).  Registers are held to eight CTAs an SM:
+// with 54 instead of 32 the first figure was 33.
+template <typename T, int NU, int GS>
+__global__ void __launch_bounds__(kThreadsW, sizeof(T) == 2 ? (NU == 4 ? 5 : 8) : NU == 1 ? 6 : 8 / NU) kv8_write_kernel(const WriteParams p) {
   pdl_enter();
   static_assert(kThreadsW == 256, "eight warps");
   __shared__ __align__(16) uint32_t s_max[2][kThreadsW / 32];
-  unsigned u = blockIdx.x;  // (which, head, j, b), which fastest
+  unsigned u = blockIdx.x;  // (which, heads, j, b), which fastest
   const bool isv = u & 1u;
   u >>= 1;
-  const int h = u % p.Hkv;
-  u /= p.Hkv;
+  const int h = (u % p.hgroups << (8 - GS)) + (GS == 8 ? 0 : threadIdx.x >> GS);
+  u /= p.hgroups;
+  constexpr int nthr = 1 << GS;
+  const int tid = threadIdx.x & (nthr - 1);  // among the head's threads
+  const bool mine = GS == 8 || h < p.Hkv;
   const int j = u % p.jmax;
   const int b = u / p.jmax;
   const int p0 = p.start[b];
   const int cnt = p.count ? max(0, min(p.count[b], p.T)) : p.T;
   if (cnt == 0) return;
   if (p0 < 0 || p0 > p.n_max - cnt) {  // not all rows fit: none is written
-    if (j == 0 && h == 0 && !isv && threadIdx.x == 0)
+    if (j == 0 && h == 0 && !isv && tid == 0)
       record_error(p.ws_header, CLSA_ERR_BAD_INDEX, ((long long)b << 32) | (unsigned)p0);
     return;
   }
@@ -165,44 +183,45 @@ __global__ void __launch_bounds__(kThreadsW) kv8_write_kernel(const WriteParams 
   const int lo = max(first, p0);           // new rows of this block: tokens [lo, hi)
   const int hi = min(first + p.block, p0 + cnt);
   const int sh = p.d == 128 ? 3 : 2, mask = (1 << sh) - 1;  // a row has 8 or 4 units
-  const int units = (hi - lo) << sh;
+  const int units = mine ? (hi - lo) << sh : 0;
   const T* src = static_cast<const T*>(isv ? p.V : p.K) + (((size_t)b * p.T + (lo - p0)) * p.Hkv + h) * p.d;
   const size_t rstr = (size_t)p.Hkv * p.d;
   uint8_t* codes = (isv ? p.V8 : p.K8) + ((size_t)b * p.n_max * p.Hkv + h) * p.d;
   float* sc = (isv ? p.vs : p.ks) + ((size_t)b * p.nblk + blk) * p.Hkv + h;
-  const bool kept = lo > first;            // the block holds earlier rows
+  const bool kept = mine && lo > first;    // the block holds earlier rows
   const float s_old = kept ? *sc : 0.f;
 
   Load16<T> x[NU];
   uint32_t mx = 0;
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int v = threadIdx.x + i * kThreadsW;
-    if (v < units) x[i].load(src + (size_t)(v >> sh) * rstr + (v & mask) * 16);
+    const int v = tid + i * nthr;
+    if (v < units) x[i].load(src + (size_t)(v >> sh) * rstr + (v & mask) * 16, p.wide);
     else x[i].zero();
   }
 #pragma unroll
   for (int i = 0; i < NU; ++i) mx = max(mx, x[i].amax());
-  mx = cta_max(mx, s_max[0]);              // also: every thread has read the old scale
-  if (mx >= 0x7f800000u) {                 // something is not finite: the largest of the rest
+  uint32_t all;
+  mx = group_max<GS>(mx, s_max[0], all);  // also: every thread has read the old scale
+  if (all >= 0x7f800000u) {                // something is not finite: the largest of the rest
     mx = 0;
 #pragma unroll
     for (int i = 0; i < NU; ++i) mx = max(mx, x[i].amax_finite());
-    mx = cta_max(mx, s_max[1]);
+    mx = group_max<GS>(mx, s_max[1], all);
   }
   float s = exp2_int(kv8_scale_exp(mx));
   if (kept) s = fmaxf(s, s_old);
   const float inv = 1.f / s;               // exact: s is a power of two
 #pragma unroll
   for (int i = 0; i < NU; ++i) {
-    const int v = threadIdx.x + i * kThreadsW;
+    const int v = tid + i * nthr;
     if (v < units) *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = x[i].codes(inv);
   }
-  if (threadIdx.x == 0 && !(kept && s == s_old)) *sc = s;
+  if (tid == 0 && mine && !(kept && s == s_old)) *sc = s;
   if (kept && s > s_old) {                 // the earlier rows move to the larger scale
     const float r = s_old * inv;
     const int old_units = (lo - first) << sh;
-    for (int v = threadIdx.x; v < old_units; v += kThreadsW) {
+    for (int v = tid; v < old_units; v += nthr) {
       uint4* at = reinterpret_cast<uint4*>(codes + (size_t)(first + (v >> sh)) * rstr + (v & mask) * 16);
       uint4 q = *at;
       uint32_t* w = reinterpret_cast<uint32_t*>(&q);
@@ -228,12 +247,14 @@ struct ReadParams {
   void* V;
   void* ws_header;
   int B, T, n_max, Hkv, d, bshift, nblk, tpc;
+  bool wide;              // K and V are 32-byte aligned
 };
 
 // A thread keeps its place in the row (threadIdx.x: 16 codes of a head, threadIdx.y: the head,
 // blockIdx.y: K or V and the heads behind blockDim.y) and walks the rows of the CTA, kReadRows of
-// them in flight: no divisions in the loop.  4 x 8001 rows of 8 x 128 as bf16: 34.1 us with two rows,
-// 38 with four, 44 with eight (more registers, fewer threads); 42 with a flat index.
+// them in flight: no divisions in the loop.  4 x 8001 rows of 8 x 128 as bf16: 31.6 us, 6.2 TB/s; 33.1
+// with stores of 16 bytes, then 38 with four rows, 44 with eight (more registers, fewer threads), 34.1
+// with one step a CTA, 34.9 with four.  One step where the CTAs all fit at once.
 constexpr int kReadRows = 2;
 template <typename T>
 __global__ void __launch_bounds__(256, 5) kv8_read_kernel(const ReadParams p) {
@@ -282,15 +303,13 @@ __global__ void __launch_bounds__(256, 5) kv8_read_kernel(const ReadParams p) {
         f[2 * e + 1] = x.y * s[i];
       }
       if constexpr (sizeof(T) == 2) {
-        uint4* o = reinterpret_cast<uint4*>(out + (size_t)ti * rstr);
+        uint32_t x[8];
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          o[q] = make_uint4(pack_bf16x2(f[8 * q], f[8 * q + 1]), pack_bf16x2(f[8 * q + 2], f[8 * q + 3]),
-                            pack_bf16x2(f[8 * q + 4], f[8 * q + 5]), pack_bf16x2(f[8 * q + 6], f[8 * q + 7]));
+        for (int e = 0; e < 8; ++e) x[e] = pack_bf16x2(f[2 * e], f[2 * e + 1]);
+        st_32(out + (size_t)ti * rstr, x, p.wide);
       } else {
-        float4* o = reinterpret_cast<float4*>(out + (size_t)ti * rstr);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[q] = make_float4(f[4 * q], f[4 * q + 1], f[4 * q + 2], f[4 * q + 3]);
+        st_32(out + (size_t)ti * rstr, reinterpret_cast<const uint32_t*>(f), p.wide);
+        st_32(out + (size_t)ti * rstr + 8, reinterpret_cast<const uint32_t*>(f) + 8, p.wide);
       }
     }
   }
@@ -303,12 +322,18 @@ int log2_of(int x) {
 }
 
 template <typename T>
-cudaError_t launch_write(const WriteParams& p, cudaStream_t s) {
-  const dim3 grid((unsigned)(2LL * p.Hkv * p.jmax * p.B));
+cudaError_t launch_write(WriteParams p, cudaStream_t s) {
+  // a block of 16 x 64 has 64 units: a CTA takes four heads (2 x 16384 rows of 8 x 64 in such blocks: 22
+  // us; 67 with a head a CTA, most of its threads idle)
+  const int units = p.block * (p.d / 16), gs = std::min(8, log2_of(units));
+  p.hgroups = (p.Hkv + (kThreadsW >> gs) - 1) >> (8 - gs);
+  const dim3 grid((unsigned)(2LL * p.hgroups * p.jmax * p.B));
+  if (gs == 6) return launch_pdl(kv8_write_kernel<T, 1, 6>, grid, dim3(kThreadsW), 0, s, p);
+  if (gs == 7) return launch_pdl(kv8_write_kernel<T, 1, 7>, grid, dim3(kThreadsW), 0, s, p);
   const int nu = (std::min(p.T, p.block) * (p.d / 16) + kThreadsW - 1) / kThreadsW;  // <= 4: 128 x 128
-  if (nu <= 1) return launch_pdl(kv8_write_kernel<T, 1>, grid, dim3(kThreadsW), 0, s, p);
-  if (nu <= 2) return launch_pdl(kv8_write_kernel<T, 2>, grid, dim3(kThreadsW), 0, s, p);
-  return launch_pdl(kv8_write_kernel<T, 4>, grid, dim3(kThreadsW), 0, s, p);
+  if (nu <= 1) return launch_pdl(kv8_write_kernel<T, 1, 8>, grid, dim3(kThreadsW), 0, s, p);
+  if (nu <= 2) return launch_pdl(kv8_write_kernel<T, 2, 8>, grid, dim3(kThreadsW), 0, s, p);
+  return launch_pdl(kv8_write_kernel<T, 4, 8>, grid, dim3(kThreadsW), 0, s, p);
 }
 
 }  // namespace
@@ -340,6 +365,7 @@ cudaError_t launch_kv8_write(const clsa_kv8_cache* c, const void* K, const void*
   p.block = c->block;
   p.nblk = (c->n_max + c->block - 1) / c->block;
   p.bshift = log2_of(c->block);
+  p.wide = (((uintptr_t)K | (uintptr_t)V) & 31) == 0;
   p.jmax = (int)write_jmax(T, c->block);
   const cudaError_t e = dt == CLSA_BF16 ? launch_write<__nv_bfloat16>(p, s) : launch_write<float>(p, s);
   launches_add(1, s);
@@ -351,10 +377,15 @@ static dim3 read_block(const clsa_kv8_cache* c) {
   const int x = c->d / 16, y = std::min(c->Hkv, 256 / x);
   return dim3(x, y, std::max(1, 256 / (x * y)));
 }
-static int read_tpc(const clsa_kv8_cache* c) { return kReadRows * (int)read_block(c).z; }
+static int read_heads(const clsa_kv8_cache* c) { return 2 * ((c->Hkv + read_block(c).y - 1) / read_block(c).y); }  // grid.y
+static int read_tpc(const clsa_kv8_cache* c, int T) {
+  const int rows = kReadRows * (int)read_block(c).z;
+  const double ctas = std::ceil((double)T / rows) * c->B * read_heads(c);
+  return ctas >= 10.0 * device_info().sm_count ? 2 * rows : rows;  // five fit on an SM
+}
 
 bool kv8_read_grid_ok(const clsa_kv8_cache* c, int T) {
-  const int tpc = read_tpc(c);
+  const int tpc = kReadRows * (int)read_block(c).z;
   return ((long long)T + tpc - 1) / tpc * c->B <= 0x7fffffffLL && c->Hkv <= 1 << 16;
 }
 
@@ -378,9 +409,10 @@ cudaError_t launch_kv8_read(const clsa_kv8_cache* c, const int32_t* start, const
   p.d = c->d;
   p.bshift = log2_of(c->block);
   p.nblk = (c->n_max + c->block - 1) / c->block;
-  p.tpc = read_tpc(c);
+  p.tpc = read_tpc(c, T);
+  p.wide = (((uintptr_t)K | (uintptr_t)V) & 31) == 0;
   const dim3 block = read_block(c);
-  const dim3 grid((unsigned)(((long long)T + p.tpc - 1) / p.tpc * c->B), 2 * ((c->Hkv + block.y - 1) / block.y));
+  const dim3 grid((unsigned)(((long long)T + p.tpc - 1) / p.tpc * c->B), read_heads(c));
   const cudaError_t e = dt == CLSA_BF16 ? launch_pdl(kv8_read_kernel<__nv_bfloat16>, grid, block, 0, s, p)
                                         : launch_pdl(kv8_read_kernel<float>, grid, block, 0, s, p);
   launches_add(1, s);

@@ -7,7 +7,7 @@ import torch
 
 from long_context_sparse_clsa_b200 import clsa
 from oracle import cache_oracle as C
-from test_gpu_cache import DT, cache_of, dev, f64
+from test_gpu_cache import DT, cache_of, dev, f64, host
 from test_gpu_cache_attn import check, check8, check_window, run8, run_window, window_reference
 
 pytestmark = pytest.mark.gpu
@@ -189,3 +189,68 @@ def test_a_workspace_serves_other_sizes_once_zeroed():
         ws.buf.zero_()
         O, lse = clsa.window_attn(Q, K[:B], V[:B], dev(lens, torch.int32), 1800, 4, ws=ws)
         check_window(Q, K[:B], V[:B], O, lse, lens, 1800, 4, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,n,H,d,block,at", [(2, 70, 100, 5, 64, 16, 7), (1, 33, 64, 3, 128, 16, 0), (3, 40, 90, 7, 64, 32, 20),
+                                               (1, 900, 1000, 1, 64, 16, 3), (2, 1, 50, 9, 64, 16, 17)])
+def test_kv8_write_several_heads_a_cta_at_any_alignment(dtype, B, T, n, H, d, block, at):
+    """Small blocks share a CTA with other heads', also where the heads do not divide; rows 16- but not
+    32-byte aligned; a value that is not finite in one head leaves the others' scales alone."""
+    g = np.random.default_rng(T)
+    off = 8 if dtype == "bf16" else 4                      # elements: 16 bytes
+    rows = []
+    for _ in range(2):
+        flat = torch.empty(B * T * H * d + off, dtype=DT[dtype], device="cuda")
+        x = flat[off:].view(B, T, H, d)
+        x.copy_(dev(g.standard_normal((B, T, H, d)) * np.exp2(g.uniform(-9, 9, (B, 1, H, 1))), DT[dtype]))
+        assert x.data_ptr() % 32 == 16
+        rows.append(x)
+    K, V = rows
+    K[0, T // 2, H - 1, 5] = float("inf")
+    V[B - 1, 0, 0, d - 1] = float("nan")
+    cache = cache_of(B, n, H, d, block, 5)
+    start = np.full(B, at)
+    start[-1] = 0
+    count = g.integers(1, T + 1, B)
+    count[0] = T
+    before = host(cache)
+    clsa.kv8_write(cache, K, V, dev(start, torch.int32), dev(count, torch.int32))
+    want = [C.kv8_write(c, s, f64(x), start, count, block) for x, c, s in ((K, before[0], before[2]), (V, before[1], before[3]))]
+    got = host(cache)
+    for side in range(2):
+        codes, scales = want[side]
+        np.testing.assert_array_equal(got[2 + side], scales)
+        nan = (got[side] & 127) == 127
+        np.testing.assert_array_equal(nan, (codes & 127) == 127)
+        np.testing.assert_array_equal(got[side][~nan], codes[~nan])
+    out = [torch.empty(B * T * H * d + off, dtype=DT[dtype], device="cuda")[off:].view(B, T, H, d).fill_(7) for _ in range(2)]
+    clsa.kv8_read(cache, *out, start=dev(start, torch.int32), count=dev(count, torch.int32))
+    al = clsa.kv8_read(cache, T=T, start=dev(start, torch.int32), dtype=DT[dtype])
+    for x, y in zip(out, al):
+        for b in range(B):
+            assert torch.equal(x[b, :count[b]].nan_to_num(-3), y[b, :count[b]].nan_to_num(-3)) and bool((x[b, count[b]:] == 7).all())
+
+
+@pytest.mark.parametrize("T,d", [(1, 128), (200, 128), (200, 64)])
+def test_attention_outputs_at_any_alignment(T, d):
+    """O, Q and the cache 16- but not 32-byte aligned: the same bits as elsewhere."""
+    g = np.random.default_rng(d)
+
+    def off(t):
+        u = torch.empty(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape)
+        assert u.data_ptr() % 32 == 16
+        return u.copy_(t)
+
+    Q = dev(g.standard_normal((2, T, 8, d)), torch.bfloat16)
+    K, V = (dev(g.standard_normal((2, 500, 2, d)), torch.bfloat16) for _ in range(2))
+    lens = dev(np.array([500, 130]), torch.int32)
+    want, wl = clsa.window_attn(Q, K, V, lens, 200, 4)
+    got, gl = clsa.window_attn(off(Q), off(K), off(V), lens, 200, 4, O=off(torch.zeros_like(Q)))
+    assert torch.equal(want, got) and torch.equal(wl, gl)
+    cache = cache_of(2, 300, 2, d, 32, 1)
+    Q = dev(g.standard_normal((1, 2, 8, d)), torch.bfloat16)
+    cnt = dev(np.array([300, 77]), torch.int32)
+    want, wl = clsa.kv8_attn(Q, cache, cnt)
+    got, gl = clsa.kv8_attn(off(Q), cache, cnt, O=off(torch.zeros_like(Q)))
+    assert torch.equal(want, got) and torch.equal(wl, gl)
