@@ -39,13 +39,16 @@
 //
 // Work split.  A unit is a (sequence, row group, KV head); the heads of the same tokens go to CTAs side by
 // side.  Few units of like length get whole CTAs each; else all units' tiles form one line that the
-// CTAs share equally, so ragged lengths balance.  A unit that several CTAs share is merged by the one that arrives last, in CTA
-// order (the result does not depend on who that is).
+// CTAs share equally, so ragged lengths balance.  A unit that several CTAs share is merged by the one
+// that arrives last, in CTA order (the result does not depend on who that is).  Many units go to a
+// warp each, which shares nothing with the others (fp32, 8 rows a unit, T = 742, W = 6: 11 us, against
+// 33 with CTAs).
 #pragma once
 
 #include <cuda.h>
 
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -183,9 +186,11 @@ template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
 
 // A variant: the kind of cache, fp32 rows, consecutive tokens through the ring (or loads into registers), head
-// dimension, row tiles.
-template <int CACHE_, bool F32_, bool RING_, int D_, int NT_>
+// dimension, row tiles; a unit per warp.
+template <int CACHE_, bool F32_, bool RING_, int D_, int NT_, bool SOLO_ = false>
 struct Cfg {
+  using Solo = Cfg<CACHE_, F32_, RING_, D_, NT_, true>;
+  static constexpr bool SOLO = SOLO_;
   static constexpr int CACHE = CACHE_, D = D_, NT = NT_;
   static constexpr bool F32 = F32_, RING = RING_;
   static constexpr int ROWS = NT * 8;
@@ -282,10 +287,17 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   int s, base = 0, r0 = 0, r1 = 1;               // item; its first tile in the line; this CTA's stretch
   int u_g = 0, u_c0 = 0, u_n = 0;                // whole: the unit's head in the line, first CTA, CTAs
   int N, P, q, rem;                              // CTA cc takes tiles [bnd(cc), bnd(cc + 1)) of N
+  // no fewer tiles a CTA than worth it, but a unit does not wait for another while CTAs are idle
+  auto ctas = [&]() { return min(PG, max((N + kMinTiles - 1) / kMinTiles, min(N, nU))); };
   auto bnd = [&](int cc) { return cc * q + min(cc, rem); };
   auto owner = [&](int t) { return t < rem * (q + 1) ? t / (q + 1) : rem + (t - rem * (q + 1)) / q; };
   Item it;
-  if (nU <= 32) {                                // every warp for itself, a lane per unit
+  constexpr bool solo = C::SOLO;
+  constexpr int stride = solo ? 1 : kWarps;         // tiles from one of a warp's to its next
+  if constexpr (solo) {                          // units r0, r0 + PG warps, ...
+    r0 = cg * kWarps + warp;
+    r1 = nU;
+  } else if (nU <= 32) {                         // every warp for itself, a lane per unit
     it.npos = 0;
     if (lane < nU) it = item_of(p, folded ? lane : lane / nh, ROWS);
     const int mine = tiles_of(it.npos);
@@ -310,7 +322,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       u_c0 = __shfl_sync(0xffffffffu, pref, u);
       u_n = __shfl_sync(0xffffffffu, want, u);
     } else {
-      P = min(PG, (N + kMinTiles - 1) / kMinTiles);
+      P = ctas();
       q = N / P;
       rem = N - q * P;
       if (cg >= P) return;
@@ -338,7 +350,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       N += sm_scan[w];
     }
     if (N == 0) return;
-    P = min(PG, (N + kMinTiles - 1) / kMinTiles);
+    P = ctas();
     q = N / P;
     rem = N - q * P;
     if (cg >= P) return;
@@ -363,9 +375,20 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
 
   while (r0 < r1) {
     // ---- the next unit (it, g): its tiles [t_beg, t_end); CTA groups c0 .. c0 + n - 1 share it -------
+    if (solo) {
+      s = folded ? r0 : r0 / nh;
+      it = item_of(p, s, ROWS);
+    }
     int nt_item = tiles_of(it.npos);
     int g, t_beg, t_end, c0, n;
-    if (whole) {
+    if (solo) {
+      g = folded ? gsub : r0 - s * nh;
+      c0 = t_beg = 0;
+      t_end = nt_item;
+      n = 1;
+      r0 += PG * kWarps;
+      if (nt_item == 0) continue;
+    } else if (whole) {
       g = folded ? gsub : u_g;
       c0 = u_c0;
       n = u_n;
@@ -542,17 +565,17 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     };
 
     if constexpr (!FP8) load_q();                // before the loads: there the registers are scarce
-    const int nw = min(kWarps, t_end - t_beg);   // warps that have a tile
-    int t = t_beg + warp, tok = -1, tok_n = -1;
+    const int nw = solo ? kWarps : min(kWarps, t_end - t_beg);  // warps that have a tile
+    int t = solo ? 0 : t_beg + warp, tok = -1, tok_n = -1;
     float sc;
     if constexpr (RING) {
 #pragma unroll
-      for (int x = 0; x < NST; ++x) issue(t + x * kWarps);
+      for (int x = 0; x < NST; ++x) issue(t + x * stride);
       tok = token(t);
       sc = load_scale(tok);
     } else {
       tok = token(t);
-      tok_n = token(t + kWarps);
+      tok_n = token(t + stride);
       if constexpr (IDX) {                       // while the indices are on their way
         if (warp < nw) load_q();
       }
@@ -563,8 +586,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     if constexpr (RING && FP8) {
       if (warp < nw) load_q();
     }
-    if (tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
-    for (; t < t_end; t += kWarps) {
+    if (!solo && tid < nr) sm_off[tid] = out_at(b, g, row0 + tid);
+    for (; t < t_end; t += stride) {
       int tok_nn = -1;
       unsigned char* stage = nullptr;
       if constexpr (RING) {
@@ -575,14 +598,14 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
         }
         ++used;
         stage = ring + slot * C::STAGE;
-        tok_n = token(t + kWarps);
+        tok_n = token(t + stride);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < KC; ++i)
             kr[h][i] = *reinterpret_cast<const uint4*>(stage + chunk(gid + 8 * h, 4 * i + tig));
       } else {
-        tok_nn = token(t + 2 * kWarps);
+        tok_nn = token(t + 2 * stride);
       }
       // S^T
       float sa[NT][4];
@@ -785,19 +808,42 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       if constexpr (RING) {
         __syncwarp();                            // the stage has been used: the next tile may overwrite it
-        issue(t + NST * kWarps);
+        issue(t + NST * stride);
       } else {
         load_v(tok_n);
       }
       tok = tok_n;
       tok_n = tok_nn;
     }
-    if constexpr (RING) {
-      if (dead) {                                // loads in flight land before their memory has another use
-        for (; used < issued; ++used) mbar_wait_warp(&sm_full[warp][used % NST], (uint32_t)(used / NST) & 1u);
-      }
-      __syncthreads();                           // the warps' outputs go over the ring
+    if (RING && dead) {                          // loads in flight land before their memory has another use
+      for (; used < issued; ++used) mbar_wait_warp(&sm_full[warp][used % NST], (uint32_t)(used / NST) & 1u);
     }
+    // float4 of a row that holds a lane's d tiles j, j + 1
+    auto chunk_of = [&](int j) { return FP8 ? gid * (D / 32) + j / 2 : CACHE == kBf16 ? 16 * (j >> 2) + 2 * gid + ((j & 3) >> 1) : 8 * (j >> 1) + gid; };
+    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
+    auto put_lse = [&](long long at, float M, float L) {
+      if (p.lse) p.lse[at / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+    };
+    if constexpr (solo) {                        // the warp has the whole unit
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) l[nt][x] += __shfl_xor_sync(0xffffffffu, l[nt][x], d);
+          const int row = nt * 8 + 2 * tig + x;
+          if (row >= nr) continue;
+          const long long at = out_at(b, g, row0 + row);
+          const float f = over_sum(m[nt][x], mv[nt][x], l[nt][x]);
+#pragma unroll
+          for (int j = 0; j < KS; j += 2)
+            store4(at + chunk_of(j) * 4, make_float4(o[nt][j][x] * f, o[nt][j][2 + x] * f, o[nt][j + 1][x] * f, o[nt][j + 1][2 + x] * f));
+          if (gid == 0) put_lse(at, m[nt][x], l[nt][x]);
+        }
+      }
+      __syncwarp();
+    } else {
+    if (RING) __syncthreads();                   // the warps' outputs go over the ring
 
     // ---- the warps' results to one -----------------------------------------------------------
     // float4 `ch` of a warp's row, placed so that neither its writers nor its readers collide
@@ -817,8 +863,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
         }
 #pragma unroll
         for (int j = 0; j < KS; j += 2) {          // two d tiles: 4 elements of d in a row
-          const int ch = FP8 ? gid * (D / 32) + j / 2
-                             : CACHE == kBf16 ? 16 * (j >> 2) + 2 * gid + ((j & 3) >> 1) : 8 * (j >> 1) + gid;
+          const int ch = chunk_of(j);
 #pragma unroll
           for (int x = 0; x < 2; ++x)
             *so(warp, nt * 8 + 2 * tig + x, ch) = make_float4(o[nt][j][x], o[nt][j][2 + x], o[nt][j + 1][x], o[nt][j + 1][2 + x]);
@@ -849,10 +894,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       return x;
     };
-    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
-    auto lse_of = [&](int row, float M, float L) {
-      if (p.lse) p.lse[sm_off[row] / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
-    };
+    auto lse_of = [&](int row, float M, float L) { put_lse(sm_off[row], M, L); };
     const int tasks = nr * (D / 4);              // float4s of the unit's rows
     if (n == 1) {
 #pragma unroll 1
@@ -985,6 +1027,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     }
     if (RING) fence_proxy_async_smem();
     __syncthreads();
+    }
   }
 }
 
@@ -995,6 +1038,13 @@ __global__ void __launch_bounds__(C::W * 32, 1) stream_attn_kernel(const __grid_
 }
 
 inline size_t counter_bytes(const Params& p) { return align_up((size_t)p.B * p.nrg * p.Hkv * 4, 256); }
+
+// the most tiles that a unit can have
+inline int most_tiles(const Params& p, int rows) {
+  long long seen = p.idx ? p.k : p.n_max;
+  if (p.T > 0) seen = std::min<long long>(seen, (long long)p.window + p.sinks + (rows - 1) / p.G + kTile);
+  return (int)((seen + kTile - 1) / kTile);
+}
 
 // the row groups of R rows: one or two row tiles
 inline int row_tiles(int R, bool f32) { return R <= 8 || f32 ? 1 : 2; }
@@ -1026,16 +1076,9 @@ size_t ws_bytes(const Params& p) {
 }
 
 template <typename C>
-cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
+cudaError_t launch_as(Params& p, cudaStream_t s) {
   const int P = std::max(1, device_info().sm_count);
-  p.counter = static_cast<uint32_t*>(ws_body);
-  p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
   Maps maps{};
-  // Heads side by side, so that the cache's rows, which hold all heads, are read whole at about the same
-  // time.  Only where few CTAs stay idle for it.
-  p.HG = p.Hkv <= P && (P % p.Hkv) * 16 <= P ? p.Hkv : 1;
-  p.nh = p.Hkv / p.HG;
-  p.PG = P / p.HG;
   if (C::RING) {
     const uint64_t rows = (uint64_t)p.seqs * p.n_max, bytes = (uint64_t)p.Hkv * C::RB;
     if (!make_map(&maps.k, p.K, rows, bytes, std::min(C::RB, 128)) || !make_map(&maps.v, p.V, rows, bytes, std::min(C::RB, 128)))
@@ -1046,6 +1089,26 @@ cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   if (e == cudaSuccess) e = launch_pdl(stream_attn_kernel<C>, dim3(P), dim3(C::W * 32), smem, s, maps, p);
   launches_add(1, s);
   return e;
+}
+
+template <typename C>
+cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
+  const int P = std::max(1, device_info().sm_count);
+  p.counter = static_cast<uint32_t*>(ws_body);
+  p.part = reinterpret_cast<float*>(static_cast<char*>(ws_body) + counter_bytes(p));
+  // Heads side by side, so that the cache's rows, which hold all heads, are read whole at about the same
+  // time.  Only where few CTAs stay idle for it.
+  p.HG = p.Hkv <= P && (P % p.Hkv) * 16 <= P ? p.Hkv : 1;
+  p.nh = p.Hkv / p.HG;
+  p.PG = P / p.HG;
+  // More units than CTAs: a unit per warp, unless its rounds fit the warps badly.  Besides its tiles, a
+  // warp's share of HBM each, a unit costs a CTA about 6.5 us and a warp 3.  (8-bit cache, 900 sequences
+  // of 512 tokens, 32 heads on 8: 181 us, 330 with CTAs; 40 of 1000: 65 and 33; 64 of 4096: 246 and 107.
+  // fp32 windows, T = 2048, W = 1024, 32 on 8: 1554 and 2134; 8 on 2, 1.7 rounds: 391 and 525.)
+  const double units = (double)p.B * p.nrg * p.nh, rounds = units / ((double)p.PG * C::W);
+  const double tiles_us = most_tiles(p, C::ROWS) * (C::STAGE * C::W / 44e3);
+  const bool solo = units > p.PG && std::ceil(rounds) * (3 + tiles_us) < rounds * (6.5 * C::W + tiles_us);
+  return solo ? launch_as<typename C::Solo>(p, s) : launch_as<C>(p, s);
 }
 
 }  // namespace stream

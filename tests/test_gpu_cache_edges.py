@@ -254,3 +254,36 @@ def test_attention_outputs_at_any_alignment(T, d):
     want, wl = clsa.kv8_attn(Q, cache, cnt)
     got, gl = clsa.kv8_attn(off(Q), cache, cnt, O=off(torch.zeros_like(Q)))
     assert torch.equal(want, got) and torch.equal(wl, gl)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,n,L,Hq,Hkv,d", [(300, 60, 1, 8, 2, 64), (90, 130, 2, 32, 8, 64), (40, 200, 1, 6, 3, 128), (260, 33, 1, 15, 15, 64),
+                                           (21, 100, 6, 12, 1, 128)])
+def test_kv8_attn_more_units_than_ctas(dtype, B, n, L, Hq, Hkv, d):
+    """Many short sequences: a warp each, empty ones among them, dense and selected; the same bits in a second
+    call."""
+    cache = cache_of(B, n, Hkv, d, 16, B)
+    g = np.random.default_rng(n)
+    counts = g.integers(0, n + 1, B)
+    counts[:3] = (n, 0, 1)
+    Q, O, lse, ws = run8(cache, L, B, Hq, dtype, counts)
+    check8(cache, Q, O, lse, counts, None, dtype)
+    O2, lse2 = clsa.kv8_attn(Q, cache, dev(counts, torch.int32), ws=ws)
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    k = min(n, 40)
+    idx = np.stack([np.sort(g.permutation(n)[:k]) for _ in range(B)])
+    counts = g.integers(0, k + 1, B)
+    Q, O, lse, ws = run8(cache, L, B, Hq, dtype, counts, idx)
+    check8(cache, Q, O, lse, counts, idx, dtype)
+    assert ws.status()[0] == "CLSA_OK"
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B,T,n,Hq,Hkv,d,window,sinks", [(1, 700, 900, 6, 3, 128, 6, 0), (3, 300, 400, 8, 2, 64, 7, 3), (200, 1, 300, 8, 2, 128, 40, 4),
+                                                        (120, 2, 200, 4, 2, 64, 150, 17), (1, 900, 1000, 16, 8, 64, 100, 1)])
+def test_window_attn_more_units_than_ctas(dtype, B, T, n, Hq, Hkv, d, window, sinks):
+    lens = np.random.default_rng(B).integers(0, n + 1, B)
+    lens[-1] = 0
+    lens[0] = n
+    out = run_window(B, T, n, Hq, Hkv, d, dtype, lens, window, sinks)
+    check_window(*out, lens, window, sinks, dtype)
