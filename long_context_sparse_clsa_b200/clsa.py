@@ -489,21 +489,24 @@ def rope(q, k, pos, rot: Optional[int] = None, layout: str = "half", theta: floa
     if x is None:
         raise ValueError("q and k are both None")
     d, dt = x.shape[-1], x.dtype
-    n_pos = pos.numel()
-    if q is not None and q_out is None:
-        q_out = torch.empty_like(q)
-    if k is not None and k_out is None:
-        k_out = torch.empty_like(k)
     Hq, Hk = (q.shape[-2] if q is not None else 0), (k.shape[-2] if k is not None else 0)
     if k is not None and k.shape[-1] != d:
         raise ValueError(f"k: head dimension {d} is wanted, got {k.shape[-1]}")
     dev, stream = _now(x, "q" if q is not None else "k")
-    a = RopeArgs(_dt(x), q.numel() // (Hq * d) if Hq else 0, k.numel() // (Hk * d) if Hk else 0, n_pos, Hq, Hk, d,
+    qa, ka = _here(q, dev, "q", None, dt), _here(k, dev, "k", None, dt)
+    if q is not None and q_out is None:
+        q_out = torch.empty_like(q)
+        qo = q_out.data_ptr()
+    else:
+        qo = _here(q_out, dev, "q_out", q.shape if q is not None else None, dt)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k)
+        ko = k_out.data_ptr()
+    else:
+        ko = _here(k_out, dev, "k_out", k.shape if k is not None else None, dt)
+    a = RopeArgs(_dt(x), q.numel() // (Hq * d) if Hq else 0, k.numel() // (Hk * d) if Hk else 0, pos.numel(), Hq, Hk, d,
                  d if rot is None else rot, _ROPE_LAYOUT[layout], _ROPE_SCALING[scaling], bool(inverse), orig_len,
-                 theta, factor, beta_fast, beta_slow, mscale, _here(q, dev, "q", None, dt), _here(k, dev, "k", None, dt),
-                 _here(pos, dev, "pos", None, torch.int32),
-                 _here(q_out, dev, "q_out", q.shape if q is not None else None, dt),
-                 _here(k_out, dev, "k_out", k.shape if k is not None else None, dt))
+                 theta, factor, beta_fast, beta_slow, mscale, qa, ka, _here(pos, dev, "pos", None, torch.int32), qo, ko)
     _check(load_library().clsa_rope(ctypes.byref(a), stream), "clsa_rope")
     return q_out, k_out
 
