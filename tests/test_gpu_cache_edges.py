@@ -287,3 +287,50 @@ def test_window_attn_more_units_than_ctas(dtype, B, T, n, Hq, Hkv, d, window, si
     lens[0] = n
     out = run_window(B, T, n, Hq, Hkv, d, dtype, lens, window, sinks)
     check_window(*out, lens, window, sinks, dtype)
+
+
+def test_a_decode_loop_back_to_back_is_the_loop_with_pauses():
+    """Positions, write, dense and window attention of 60 steps in a row, one launch behind the other, eager and
+    captured: every step reads what the launch before it wrote."""
+    g = np.random.default_rng(4)
+    B, Hq, H, d, steps, n0 = 3, 8, 2, 128, 60, 500
+    Q = dev(g.standard_normal((steps, B, Hq, d)), torch.bfloat16)
+    Kn, Vn = (dev(g.standard_normal((steps, B, 1, H, d)) * np.exp2(g.uniform(-3, 3, (steps, B, 1, 1, 1))), torch.bfloat16) for _ in range(2))
+    K0, V0 = (dev(g.standard_normal((B, n0, H, d)), torch.bfloat16) for _ in range(2))
+    zero, lens = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.full((B,), n0, dtype=torch.int32, device="cuda")
+    wws, aws, kws = clsa.Workspace(1 << 22), clsa.Workspace(1 << 22), clsa.Workspace(256)
+
+    def loop(pause, O, W, pos):
+        cache = clsa.Kv8Cache.empty(B, n0 + steps, H, d, 32)
+        Kb, Vb = (torch.zeros(B, n0 + steps, H, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        clsa.kv8_write(cache, K0, V0, zero, ws=kws)
+        pos.copy_(lens)
+        for t in range(steps):
+            q, k = clsa.rope(Q[t], Kn[t].view(B, H, d), pos)
+            pause()
+            clsa.kv8_write(cache, k.view(B, 1, H, d), Vn[t], pos, ws=kws)
+            pause()
+            clsa.kv8_read(cache, Kb, Vb, ws=kws)
+            pause()
+            pos += 1
+            pause()
+            clsa.kv8_attn(q, cache, pos, ws=aws, O=O[t], want_lse=False)
+            pause()
+            clsa.window_attn(q.view(B, 1, Hq, d), Kb, Vb, pos, 200, 2, ws=wws, O=W[t].view(B, 1, Hq, d), want_lse=False)
+            pause()
+
+    outs = []
+    for pause in (torch.cuda.synchronize, lambda: None):
+        O, W, pos = torch.empty_like(Q), torch.empty_like(Q), lens.clone()
+        loop(pause, O, W, pos)
+        outs.append((O, W))
+    O, W, pos = torch.empty_like(Q), torch.empty_like(Q), lens.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        loop(lambda: None, O, W, pos)
+    for _ in range(3):
+        graph.replay()
+        outs.append((O.clone(), W.clone()))
+    torch.cuda.synchronize()
+    for o, w in outs[1:]:
+        assert torch.equal(o, outs[0][0]) and torch.equal(w, outs[0][1])
