@@ -7,9 +7,9 @@
 // 16 tokens, multiplies them on the tensor core (mma.sync m16n8k16; a 128-row tcgen05 tile would be
 // empty for G = 4) and keeps a running maximum, sum and output for its rows.  Consecutive tokens
 // come by TMA through a ring of the warp's own in shared memory (three tiles ahead: 147 KB in flight
-// on an SM at d = 128); an index list's, and fp32 ones, by plain loads into the registers that
-// feed the tensor core, one tile ahead (an index list through a ring of asynchronous copies
-// took 17.4 us for 24 layers and 2048 tokens, by loads 16.3).
+// on an SM at d = 128); an index list's by plain loads into the registers that feed the tensor
+// core, one tile ahead (through a ring of asynchronous copies 24 layers over 2048 tokens took
+// 17.4 us, by loads 16.3).
 // Measured (32 heads on 8, d = 128): 131072 tokens of the 8-bit cache 49.5 us, 5.4 TB/s, of which the
 // loop takes 41, at the rate of a plain copy, and 8 go to the launch, the plan and the merge; 16
 // sequences of 16K to 128K tokens 277 us, 6.1 TB/s; 1028 bf16 tokens of 16 sequences 13.2 us; 24 layers
@@ -30,7 +30,8 @@
 // accumulated from 2^(s_j + e_j - n) with a reference n of its own, so halves never lose a
 // block of small scale.  With fp32 queries Q and P are split into two halves each (22 bits).
 // fp32 cache.  Every factor is the exact sum of three bf16 parts; six of the nine products
-// of parts are formed (the others are below 2^-24).
+// of parts are formed (the others are below 2^-24).  The parts of K and V cost more than the products,
+// so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8: 1297 us; 1550 with 8).
 //
 // The reference (of sums and of outputs) moves only when a score exceeds it by 2^8; then the
 // sums are rescaled.  A row's largest p is at least 2^0, at most 2^8: no overflow.  Where p becomes
@@ -197,9 +198,10 @@ struct Cfg {
   static constexpr int ES = CACHE == kE4m3 ? 1 : CACHE == kBf16 ? 2 : 4;  // bytes of a cache element
   static constexpr int RB = D * ES;                                       // bytes of a token's row
   static constexpr int STAGE = 2 * kTile * RB;                            // K and V of a tile
-  // warps of a CTA (one CTA per SM): what the registers allow.  One large CTA rather than
-  // three small: a unit that all SMs share has a third of the partials to merge.
-  static constexpr int W = RING ? (NT == 2 ? 8 : 12) : (NT == 1 && CACHE != kFp32 ? 12 : 8);
+  // warps of a CTA (one CTA per SM): what the registers allow (fp32 at d = 128: what leaves room for two
+  // ring tiles a warp).  One large CTA rather than three small: a unit that all SMs share has a third
+  // of the partials to merge.
+  static constexpr int W = CACHE == kFp32 && D == 128 ? 6 : NT == 2 || CACHE == kFp32 ? 8 : 12;
   // ring tiles of a warp: three (50.8 us over 128K tokens; 53.0 with four, 51.0 with two), or what there is room for
   static constexpr int ROOM = 192 * 1024 / (W * STAGE);
   static constexpr int NST = RING ? (ROOM < 3 ? ROOM : 3) : 1;
@@ -216,6 +218,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
   constexpr bool F32 = C::F32, RING = C::RING, FP8 = CACHE == kE4m3, IDX = FP8 && !RING;
   static_assert(F32 ? CACHE != kBf16 : CACHE != kFp32, "bf16 cache: bf16 rows; fp32 cache: fp32 rows");
   static_assert(!RING || NST >= 2, "a ring of two tiles at least");
+  static_assert(RING || FP8, "index lists: the 8-bit cache");
   constexpr int kWarps = C::W, kThreads = kWarps * 32;
   constexpr int KC = D * ES / 64;              // 16-byte chunks of a token's row that a lane takes
   constexpr int KS = D / 16;                   // k steps of S, d tiles of O
@@ -1104,7 +1107,7 @@ cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   // More units than CTAs: a unit per warp, unless its rounds fit the warps badly.  Besides its tiles, a
   // warp's share of HBM each, a unit costs a CTA about 6.5 us and a warp 3.  (8-bit cache, 900 sequences
   // of 512 tokens, 32 heads on 8: 181 us, 330 with CTAs; 40 of 1000: 65 and 33; 64 of 4096: 246 and 107.
-  // fp32 windows, T = 2048, W = 1024, 32 on 8: 1554 and 2134; 8 on 2, 1.7 rounds: 391 and 525.)
+    // fp32 windows of 8 rows a unit, T = 2048, W = 1024, 32 on 8: 1554 and 2134; 8 on 2, 1.7 rounds: 391 and 525.)
   const double units = (double)p.B * p.nrg * p.nh, rounds = units / ((double)p.PG * C::W);
   const double tiles_us = most_tiles(p, C::ROWS) * (C::STAGE * C::W / 44e3);
   const bool solo = units > p.PG && std::ceil(rounds) * (3 + tiles_us) < rounds * (6.5 * C::W + tiles_us);

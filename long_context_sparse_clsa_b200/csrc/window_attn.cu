@@ -28,7 +28,7 @@ stream::Params params_of(const clsa_window_args* a, float scale) {
   p.window = std::min(a->window, a->n_max);
   p.sinks = std::min(a->sinks, a->n_max);
   p.scale_log2 = scale * 1.4426950408889634f;
-  const int rows = 8 * stream::row_tiles(p.R, a->dtype == CLSA_F32);
+  const int rows = 8 * stream::row_tiles(p.R, false);
   p.nrg = (p.R + rows - 1) / rows;
   return p;
 }
@@ -37,9 +37,12 @@ stream::Params params_of(const clsa_window_args* a, float scale) {
 template <typename F>
 auto dispatch(const clsa_window_args* a, int R, F&& f) {
   using namespace stream;
-  const bool d128 = a->d == 128;
-  if (a->dtype == CLSA_F32) return d128 ? f(Cfg<kFp32, true, false, 128, 1>{}) : f(Cfg<kFp32, true, false, 64, 1>{});
-  if (row_tiles(R, false) == 1) return d128 ? f(Cfg<kBf16, false, true, 128, 1>{}) : f(Cfg<kBf16, false, true, 64, 1>{});
+  const bool d128 = a->d == 128, one = row_tiles(R, false) == 1;
+  if (a->dtype == CLSA_F32) {
+    if (one) return d128 ? f(Cfg<kFp32, true, true, 128, 1>{}) : f(Cfg<kFp32, true, true, 64, 1>{});
+    return d128 ? f(Cfg<kFp32, true, true, 128, 2>{}) : f(Cfg<kFp32, true, true, 64, 2>{});
+  }
+  if (one) return d128 ? f(Cfg<kBf16, false, true, 128, 1>{}) : f(Cfg<kBf16, false, true, 64, 1>{});
   return d128 ? f(Cfg<kBf16, false, true, 128, 2>{}) : f(Cfg<kBf16, false, true, 64, 2>{});
 }
 
