@@ -29,9 +29,12 @@
 // row's largest).  The value blocks' scales 2^e go into the exponent: the output is
 // accumulated from 2^(s_j + e_j - n) with a reference n of its own, so halves never lose a
 // block of small scale.  With fp32 queries Q and P are split into two halves each (22 bits).
+// fp32 rows.  The tensor core cuts its sums off instead of rounding them, always towards zero; over many
+// tiles that adds up (6e-6 of the result over 700 tokens, 4e-7 as it is).  So a tile's products are added to the
+// output, and 16 of d to the score, by fp32 additions.
 // fp32 cache.  Every factor is the exact sum of three bf16 parts; six of the nine products
 // of parts are formed (the others are below 2^-24).  The parts of K and V cost more than the products,
-// so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8: 1297 us; 1550 with 8).
+// so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8: 1345 us; 1550 with 8).
 //
 // The reference (of sums and of outputs) moves only when a score exceeds it by 2^8; then the
 // sums are rescaled.  A row's largest p is at least 2^0, at most 2^8: no overflow.  Where p becomes
@@ -168,6 +171,9 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
   hi = __byte_perm(__float_as_uint(hx), __float_as_uint(hy), 0x7632u);
   mid = __byte_perm(__float_as_uint(mx), __float_as_uint(my), 0x7632u);
   lo = __byte_perm(__float_as_uint(rx - mx), __float_as_uint(ry - my), 0x7632u);
+}
+__device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
+  a[0] += b[0], a[1] += b[1], a[2] += b[2], a[3] += b[3];
 }
 // the products of parts that reach 2^-24 of the whole, small ones first
 __device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
@@ -610,10 +616,14 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       } else {
         tok_nn = token(t + 2 * stride);
       }
-      // S^T
-      float sa[NT][4];
+      // S^T (fp32 rows: the first parts' products of 16 of d by themselves, added up in fp32; the others, which
+      // are small, in the tensor core)
+      float sa[NT][4], rest[F32 ? NT : 1][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sa[nt][0] = sa[nt][1] = sa[nt][2] = sa[nt][3] = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        sa[nt][0] = sa[nt][1] = sa[nt][2] = sa[nt][3] = 0.f;
+        if constexpr (F32) rest[nt][0] = rest[nt][1] = rest[nt][2] = rest[nt][3] = 0.f;
+      }
 #pragma unroll
       for (int i = 0; i < KC; ++i) {
         const uint32_t w0[4] = {kr[0][i].x, kr[0][i].y, kr[0][i].z, kr[0][i].w};
@@ -626,8 +636,14 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
             e4m3x4_to_f16x4(w1[w], a[1], a[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-              for (int x = 0; x < NQ; ++x) mma_f16_16816(sa[nt], a, qb[x][nt][4 * i + w][0], qb[x][nt][4 * i + w][1]);
+              if constexpr (F32) {
+                mma_f16_16816(rest[nt], a, qb[1][nt][4 * i + w][0], qb[1][nt][4 * i + w][1]);
+                float t[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16_16816(t, a, qb[0][nt][4 * i + w][0], qb[0][nt][4 * i + w][1]);
+                add4(sa[nt], t);
+              } else {
+                mma_f16_16816(sa[nt], a, qb[0][nt][4 * i + w][0], qb[0][nt][4 * i + w][1]);
+              }
             }
           }
         } else if constexpr (CACHE == kFp32) {
@@ -640,7 +656,10 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int x = 0; x < 6; ++x) mma_bf16_16816(sa[nt], a[kTermA[x]], qb[kTermB[x]][nt][i][0], qb[kTermB[x]][nt][i][1]);
+            for (int x = 0; x < 5; ++x) mma_bf16_16816(rest[nt], a[kTermA[x]], qb[kTermB[x]][nt][i][0], qb[kTermB[x]][nt][i][1]);
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16_16816(t, a[0], qb[0][nt][i][0], qb[0][nt][i][1]);
+            add4(sa[nt], t);
           }
         } else {
 #pragma unroll
@@ -673,6 +692,10 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
         }
       } else {
         load_k(tok_n);
+      }
+      if constexpr (F32) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) add4(sa[nt], rest[nt]);
       }
       // scores of tokens gid, gid + 8 (h) and rows 2 tig, 2 tig + 1 (x): sa[nt][2 h + x]
       const int tk[2] = {__shfl_sync(0xffffffffu, tok, gid), __shfl_sync(0xffffffffu, tok, gid + 8)};
@@ -759,9 +782,13 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       auto pv = [&](int j, const uint32_t (&a)[4]) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (FP8) {
-#pragma unroll
-            for (int x = 0; x < NQ; ++x) mma_f16_16816(o[nt][j], a, pb[x][nt][0], pb[x][nt][1]);
+          if constexpr (F32) {                   // a tile by itself, small parts first
+            float t[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16_16816(t, a, pb[1][nt][0], pb[1][nt][1]);
+            mma_f16_16816(t, a, pb[0][nt][0], pb[0][nt][1]);
+            add4(o[nt][j], t);
+          } else if constexpr (FP8) {
+            mma_f16_16816(o[nt][j], a, pb[0][nt][0], pb[0][nt][1]);
           } else {
             mma_bf16_16816(o[nt][j], a, pb[0][nt][0], pb[0][nt][1]);
           }
@@ -784,8 +811,10 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              float t[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-              for (int x = 0; x < 6; ++x) mma_bf16_16816(o[nt][2 * i + w], a[kTermA[x]], pb[kTermB[x]][nt][0], pb[kTermB[x]][nt][1]);
+              for (int x = 0; x < 6; ++x) mma_bf16_16816(t, a[kTermA[x]], pb[kTermB[x]][nt][0], pb[kTermB[x]][nt][1]);
+              add4(o[nt][2 * i + w], t);
             }
           }
         } else

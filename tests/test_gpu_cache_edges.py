@@ -8,7 +8,7 @@ import torch
 from long_context_sparse_clsa_b200 import clsa
 from oracle import cache_oracle as C
 from test_gpu_cache import DT, cache_of, dev, f64, host
-from test_gpu_cache_attn import check, check8, check_window, run8, run_window, window_reference
+from test_gpu_cache_attn import U, check, check8, check_window, run8, run_window, window_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -334,3 +334,33 @@ def test_a_decode_loop_back_to_back_is_the_loop_with_pauses():
     torch.cuda.synchronize()
     for o, w in outs[1:]:
         assert torch.equal(o, outs[0][0]) and torch.equal(w, outs[0][1])
+
+
+@pytest.mark.parametrize("T,d", [(888, 128), (1184, 64), (1, 128), (40, 64)])
+def test_fp32_sums_are_rounded_not_cut_off(T, d):
+    """Means of 3000 positive values (Q = 0: every p is 1).  A tile's products are cut off at 24 bits at most 6
+    times (12 u), added to the output n / 16 times (u each), the sum of p 32 at a time; merging, the division
+    and the result's rounding: 64 u are plenty.  Sums that the tensor core cuts off all the way lose 6 n / 16
+    times up to 2 u, all in one direction."""
+    g = np.random.default_rng(d)
+    n, W = 4000, 3000
+    K = dev(g.standard_normal((1, n, 1, d)))
+    V = dev(g.uniform(0.5, 1, (1, n, 1, d)))
+    Q = torch.zeros(1, T, 16, d, device="cuda")
+    O, lse = clsa.window_attn(Q, K, V, dev(np.array([n]), torch.int32), W)
+    c = torch.cat([torch.zeros(1, d, dtype=torch.float64, device="cuda"), V[0, :, 0].double().cumsum(0)])
+    p = torch.arange(n - T, n, device="cuda")
+    want = ((c[p + 1] - c[p + 1 - W]) / W)[:, None]
+    err = ((O[0].double() - want).abs() / want).max()
+    assert float(err) <= (W / 16 + 64) * U, float(err) / U
+    # the same mean over an 8-bit cache of which every token is seen
+    cache = clsa.Kv8Cache.empty(1, W, 1, d, 16)
+    codes = g.integers(0x30, 0x38, (1, W, 1, d))                # 0.5 to 0.9375
+    cache.V8.view(torch.uint8).copy_(dev(codes, torch.uint8))
+    cache.k_scale.fill_(1.0)
+    cache.v_scale.fill_(1.0)
+    B = max(T, 2)
+    O, _ = clsa.kv8_attn(torch.zeros(1, B, 8, d, device="cuda"), cache, torch.full((B,), W, dtype=torch.int32, device="cuda"))
+    want = cache.V8.double().mean(1)[0, 0]
+    err = ((O[0].double() - want).abs() / want).max()
+    assert float(err) <= (W / 16 + 64) * U, float(err) / U
