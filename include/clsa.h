@@ -307,9 +307,9 @@ CLSA_API clsa_status clsa_rope(const clsa_rope_args* a, void* stream);
 /* K8, V8 [B][n_max][Hkv][d] hold e4m3 codes, k_scale, v_scale [B][ceil(n_max / block)][Hkv]
  * fp32 a scale for each block of tokens and head: a code stands for code * scale.  The scale
  * is the smallest power of two >= 2^-100 with max |x| / scale <= 448 over the block's finite
- * elements (at most 2^119).  block in {16, 32, 64, 128}, d in {64, 128}.  The caller owns the
- * four buffers; they need no initial value: a block's bytes are read only for rows that
- * were written. */
+ * elements (at most 2^119).  block in {16, 32, 64, 128}, d in {64, 128}, n_max <= 2^30,
+ * Hkv <= 2^16.  The caller owns the four buffers; they need no initial value: a block's bytes
+ * are read only for rows that were written. */
 typedef struct clsa_kv8_cache {
   int B, n_max, Hkv, d, block;
   void* K8;                  /* [B][n_max][Hkv][d] e4m3, 16-byte aligned          */
@@ -382,7 +382,7 @@ CLSA_API clsa_status clsa_kv8_attn(const clsa_kv8_attn_args* a, void* ws, size_t
  * can reach other rows of the call too (0 * NaN); K's stay with the rows that see them.
  * O [B][T][Hq][d] and lse [B][T][Hq] (fp32, natural log, may be NULL) out; query head h reads
  * KV head h / (Hq / Hkv).  dtype bf16 or fp32 (fp32 products).  Deterministic.  One launch.
- * CLSA_ERR_UNSUPPORTED: Hq no multiple of Hkv or Hq / Hkv > 128, T Hq > 2^27, B T Hq > 2^30, B n_max > 2^31 - 4096,
+ * CLSA_ERR_UNSUPPORTED: Hq no multiple of Hkv or Hq / Hkv > 128, Hkv > 2^16, T Hq > 2^27, B T Hq > 2^30, B n_max > 2^31 - 4096,
  * or over 2e9 tiles of 16 tokens by 8 rows of a KV head.
  * ws: clsa_window_attn_workspace_size(a) bytes (0: arguments the call would reject). */
 typedef struct clsa_window_args {

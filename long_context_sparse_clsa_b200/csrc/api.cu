@@ -145,7 +145,7 @@ clsa_status check_window(const clsa_window_args* a) {
   if (!dtype_ok(a->dtype)) return CLSA_ERR_INVALID_ARG;
   if (!a->Q || !a->K || !a->V || !a->seq_lens || !a->O) return CLSA_ERR_INVALID_ARG;
   if (!dims_ok(a->d) || a->Hq % a->Hkv != 0 || a->Hq / a->Hkv > 128) return CLSA_ERR_UNSUPPORTED;
-  if (a->n_max > (1 << 30) || a->T > (1 << 30)) return CLSA_ERR_UNSUPPORTED;
+  if (a->n_max > (1 << 30) || a->T > (1 << 30) || a->Hkv > (1 << 16)) return CLSA_ERR_UNSUPPORTED;
   if ((long long)a->T * a->Hq > 8 * kMaxStreamRows || (long long)a->B * a->T * a->Hq > 64 * kMaxStreamRows)
     return CLSA_ERR_UNSUPPORTED;
   // tiles of 16 tokens over all (sequence, 8 rows, KV head) units

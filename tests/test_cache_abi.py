@@ -155,3 +155,12 @@ def test_rope_refuses_frequencies_out_of_range(lib):
     for kw in ({"scaling": 1, "factor": 1e-310}, {"scaling": 1, "factor": 1e-17}, {"scaling": 2, "factor": 1e-300},
                {"scaling": 3, "factor": 1e-300, "orig_len": 1}):
         assert lib.clsa_rope(ctypes.byref(rope_args(**kw)), NULL) == INVALID, kw
+
+
+def test_head_counts_behind_the_range_are_refused(lib):
+    for h, want in (((1 << 16) + 1, UNSUPPORTED), (1 << 16, WORKSPACE)):
+        assert lib.clsa_window_attn(ctypes.byref(window_args(B=1, T=1, n_max=4, Hq=h, Hkv=h)), P, 0, NULL) == want
+        c = cache(B=1, n_max=4, Hkv=h)
+        assert lib.clsa_kv8_attn(ctypes.byref(attn_args(B=1, Hq=h, cache=c)), P, 0, NULL) == want
+        assert lib.clsa_kv8_write(ctypes.byref(c), P, P, P, NULL, 1, 1, P, 0, NULL) == want
+        assert lib.clsa_kv8_read(ctypes.byref(c), NULL, NULL, NULL, 1, 1, P, P, P, 0, NULL) == want
