@@ -29,6 +29,8 @@
 // row's largest).  The value blocks' scales 2^e go into the exponent: the output is
 // accumulated from 2^(s_j + e_j - n) with a reference n of its own, so halves never lose a
 // block of small scale.  With fp32 queries Q and P are split into two halves each (22 bits).
+// bf16 rows.  P is rounded to the type of V's operand, halves (2^-12) or bf16 (2^-9 of a weight, which on random
+// values adds to the result at most what its own rounding does); the row's sum takes it as it was.
 // fp32 rows.  The tensor core cuts its sums off instead of rounding them, always towards zero; over many
 // tiles that adds up (6e-6 of the result over 700 tokens, 4e-7 as it is).  So a tile's products are added to the
 // output, and 16 of d to the score, by fp32 additions.

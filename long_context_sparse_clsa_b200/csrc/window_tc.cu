@@ -24,6 +24,9 @@
 // item too) is issued right behind P V, which the in-order tensor pipe keeps from
 // overwriting P early.  m is a reference that moves only when a score exceeds it by 2^8;
 // then O is rescaled in TMEM.  A row's softmax needs no exchange: its 128 scores are one lane.
+// P is rounded to bf16, since an MMA's operands have one type and V's is bf16: up to 2^-9 of each weight,
+// which on random values adds to the result at most what its own rounding to bf16 does.  The row's sum
+// takes the weights as they were.
 // Bound: per token tile and row tile 2 x 128 x 128 x d multiplies and 128 x 128 exponentials, which at
 // d = 128 take the tensor cores and the special-function units about 1024 cycles each.
 // Measured (32 heads on 8, d = 128): T = 16381, W = 4096 840 us, 1.15 PFLOP/s of visible products; T = 4096,
