@@ -207,8 +207,10 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   uint64_t* s_full = bars + 20;
   uint64_t* p_full = bars + 22;              // [2][2]: the halves of P
   uint64_t* o_full = bars + 26;
-  // a V tile's unseen rows are zero; such tiles take the four in turn (the ring holds at most four V
-  // tiles, so the warp that zeroes them is never a whole turn ahead)
+  // a V tile's unseen rows are zero; such tiles take the four in turn.  The ring holds at most four V
+  // tiles, so the warp that zeroes them is never a whole turn ahead; nor is it one behind: a tile's slot is
+  // filled again only when this warp, too, has gone past it (its waits are by parity, and a phase that
+  // it missed would stand still).
   uint64_t* fixed = bars + 28;               // [4]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 32);
   const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::slots; ++i) {
       mbar_init(kv_full + i, 1);
-      mbar_init(kv_empty + i, 1);
+      mbar_init(kv_empty + i, 2);  // the products that read the tile, and the warp that zeroes its unseen rows
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full + i, 1);
@@ -308,21 +310,27 @@ __global__ void __launch_bounds__(kThreadsW, 1) window_tc_kernel(const __grid_co
       const WItem w = witem(p, i);
       for (int j = 0; j < w.nkv && ok; ++j, n += 2) {
         // every phase in its turn (a wait for a phase that lies two ahead would pass at once)
-        for (int x = n; x < n + 2 && ok; ++x)
+        for (int x = n; x < n + 2 && ok; ++x) {
           ok = wait_full(kv_full + x % S::slots, (uint32_t)(x / S::slots) & 1u, p.ws_header, 72);
-        int a0, a1, b0;
-        if (!ok || !dead_rows(w, j, a0, a1, b0)) continue;
-        unsigned char* v = base + S::ring + ((n + 1) % S::slots) * S::tile;
-        for (int x = lane; x < (a1 - a0 + kTok - b0) * 8; x += 32) {
-          const int r = x >> 3, row = r < a1 - a0 ? a0 + r : b0 + r - (a1 - a0);
-#pragma unroll
-          for (int a = 0; a < S::KA; ++a)
-            *reinterpret_cast<uint4*>(v + a * kAtom + row * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          if (ok && x == n && lane == 0) mbar_arrive(kv_empty + x % S::slots);
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(fixed + (nfix & 3));
-        ++nfix;
+        if (!ok) break;
+        const int slot = (n + 1) % S::slots;
+        int a0, a1, b0;
+        if (dead_rows(w, j, a0, a1, b0)) {
+          unsigned char* v = base + S::ring + slot * S::tile;
+          for (int x = lane; x < (a1 - a0 + kTok - b0) * 8; x += 32) {
+            const int r = x >> 3, row = r < a1 - a0 ? a0 + r : b0 + r - (a1 - a0);
+#pragma unroll
+            for (int a = 0; a < S::KA; ++a)
+              *reinterpret_cast<uint4*>(v + a * kAtom + row * 128 + (x & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(fixed + (nfix & 3));
+          ++nfix;
+        }
+        if (lane == 0) mbar_arrive(kv_empty + slot);
       }
     }
   } else if (warp == kMmaWarp) {
