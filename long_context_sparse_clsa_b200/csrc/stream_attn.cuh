@@ -854,7 +854,12 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     }
     // float4 of a row that holds a lane's d tiles j, j + 1
     auto chunk_of = [&](int j) { return FP8 ? gid * (D / 32) + j / 2 : CACHE == kBf16 ? 16 * (j >> 2) + 2 * gid + ((j & 3) >> 1) : 8 * (j >> 1) + gid; };
-    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? 0.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
+    // a row's outputs over its sum: x times over_sum(); -1 where it saw nothing, and then 0, not 0 * x: x is NaN
+    // beside a value of another row that is not finite
+    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? -1.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
+    auto times = [](float4 x, float f) {
+      return f < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    };
     auto put_lse = [&](long long at, float M, float L) {
       if (p.lse) p.lse[at / D] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
     };
@@ -871,7 +876,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
           const float f = over_sum(m[nt][x], mv[nt][x], l[nt][x]);
 #pragma unroll
           for (int j = 0; j < KS; j += 2)
-            store4(at + chunk_of(j) * 4, make_float4(o[nt][j][x] * f, o[nt][j][2 + x] * f, o[nt][j + 1][x] * f, o[nt][j + 1][2 + x] * f));
+            store4(at + chunk_of(j) * 4, times(make_float4(o[nt][j][x], o[nt][j][2 + x], o[nt][j + 1][x], o[nt][j + 1][2 + x]), f));
           if (gid == 0) put_lse(at, m[nt][x], l[nt][x]);
         }
       }
@@ -934,10 +939,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
 #pragma unroll 1
       for (int i = tid; i < tasks; i += kThreads) {
         float M, Mv, L;
-        float4 x = warps_sum(i, M, Mv, L);
-        const float f = over_sum(M, Mv, L);
-        x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-        store4(sm_off[i / (D / 4)] + (i % (D / 4)) * 4, x);
+        const float4 x = warps_sum(i, M, Mv, L);
+        store4(sm_off[i / (D / 4)] + (i % (D / 4)) * 4, times(x, over_sum(M, Mv, L)));
         if (i % (D / 4) == 0) lse_of(i / (D / 4), M, L);
       }
       if (RING) fence_proxy_async_smem();        // before the next unit's TMA writes
@@ -1040,8 +1043,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
               }
             }
           }
-          const float f = sm_f[row];
-          x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+          x = times(x, sm_f[row]);
           if (S > 1) sums[sl * tasks + i] = x;
           else store4(sm_off[row] + (i % (D / 4)) * 4, x);
         }
