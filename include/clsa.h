@@ -349,7 +349,7 @@ CLSA_API clsa_status clsa_kv8_read(const clsa_kv8_cache* cache, const int32_t* s
  * and CLSA_ERR_BAD_INDEX is recorded in ws (detail: b << 32 | position).
  * cache.B is B, or 1: then the one cache serves every b (rows of a prefill chunk, each with
  * its own count or selection).  A row that sees no token gets O = 0 and lse = -inf.
- * Scales are taken to be powers of two, as clsa_kv8_write makes them.  Scores, sums and outputs
+ * Scales are 0 or numbers from 2^-100 to 2^119 (clsa_kv8_write's are powers of two).  Scores, sums and outputs
  * accumulate in fp32; probabilities enter the second product as halves relative to the row's
  * largest (two halves, 22 bits, for fp32).  Deterministic.  One launch.
  * CLSA_ERR_UNSUPPORTED: Hq no multiple of Hkv, L Hq > 2^24, B L Hq > 2^27, cache.B n_max > 2^31 - 4096, or

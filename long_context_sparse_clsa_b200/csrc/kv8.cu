@@ -113,6 +113,16 @@ template <> struct Load16<float> {
   }
 };
 
+// four elements
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  float4 x;
+  unpack_bf16x2(v.x, x.x, x.y);
+  unpack_bf16x2(v.y, x.z, x.w);
+  return x;
+}
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+
 // the largest of the values of this thread's group of 2^GS threads, and of all groups; `s_max` is free
 // again behind the caller's next barrier
 template <int GS>
@@ -211,15 +221,25 @@ __global__ void __launch_bounds__(kThreadsW, sizeof(T) == 2 ? (NU == 4 ? 5 : 8) 
   }
   float s = exp2_int(kv8_scale_exp(mx));
   if (kept) s = fmaxf(s, s_old);
-  const float inv = 1.f / s;               // exact: s is a power of two
+  const float inv = 1.f / s;               // exact where s is a power of two: all but a kept scale of another program
+  if ((__float_as_uint(s) & 0x7fffffu) == 0u) {
 #pragma unroll
-  for (int i = 0; i < NU; ++i) {
-    const int v = tid + i * nthr;
-    if (v < units) *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = x[i].codes(inv);
+    for (int i = 0; i < NU; ++i) {
+      const int v = tid + i * nthr;
+      if (v < units) *reinterpret_cast<uint4*>(codes + (size_t)(lo + (v >> sh)) * rstr + (v & mask) * 16) = x[i].codes(inv);
+    }
+  } else {                                 // rare: by division, the rows read again (the registers above are all taken)
+#pragma unroll 1
+    for (int i = tid; i < 4 * units; i += nthr) {
+      const int row = i >> (sh + 2), col = (i & (4 * mask + 3)) * 4;
+      const float4 y = load4(src + (size_t)row * rstr + col);
+      *reinterpret_cast<uint32_t*>(codes + (size_t)(lo + row) * rstr + col) =
+          e4m3x4(__fdiv_rn(y.x, s), __fdiv_rn(y.y, s), __fdiv_rn(y.z, s), __fdiv_rn(y.w, s));
+    }
   }
   if (tid == 0 && mine && !(kept && s == s_old)) *sc = s;
   if (kept && s > s_old) {                 // the earlier rows move to the larger scale
-    const float r = s_old * inv;
+    const float r = s_old * inv;           // exact: s is new
     const int old_units = (lo - first) << sh;
     for (int v = tid; v < old_units; v += nthr) {
       uint4* at = reinterpret_cast<uint4*>(codes + (size_t)(first + (v >> sh)) * rstr + (v & mask) * 16);

@@ -28,7 +28,8 @@
 // Q is brought to half range by a power of two per row (exact but for elements 2^-28 of the
 // row's largest).  The value blocks' scales 2^e go into the exponent: the output is
 // accumulated from 2^(s_j + e_j - n) with a reference n of its own, so halves never lose a
-// block of small scale.  With fp32 queries Q and P are split into two halves each (22 bits).
+// block of small scale.  e is whole for the powers of two that the cache's own write makes; of any other scale
+// it has a fraction (bf16 rows), or what is left of it multiplies the weight (fp32 rows).  With fp32 queries Q and P are split into two halves each (22 bits).
 // bf16 rows.  P is rounded to the type of V's operand, halves (2^-12) or bf16 (2^-9 of a weight, which on random
 // values adds to the result at most what its own rounding does); the row's sum takes it as it was.
 // fp32 rows.  The tensor core cuts its sums off instead of rounding them, always towards zero; over many
@@ -190,6 +191,18 @@ __device__ __forceinline__ int warp_scan_int(int v, int lane) {  // sum over the
   return v;
 }
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
+
+// 2^x, subnormal results kept: all the value scales of a row may be 2^-100 and less
+__device__ __forceinline__ float exp2_gradual(float x) {
+  const bool low = x < -64.f;
+  return fast_exp2(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
+}
+// log2 by the hardware approximation: exact for powers of two (test_gpu_kv8_scales.py), -inf for 0 and subnormals
+__device__ __forceinline__ float fast_log2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <int D, int NT>
 constexpr int slot_floats() { return NT * 8 * (D + 3); }
@@ -701,13 +714,21 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
       }
       // scores of tokens gid, gid + 8 (h) and rows 2 tig, 2 tig + 1 (x): sa[nt][2 h + x]
       const int tk[2] = {__shfl_sync(0xffffffffu, tok, gid), __shfl_sync(0xffffffffu, tok, gid + 8)};
-      float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
+      float kf[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f}, vf[2] = {1.f, 1.f};
       if constexpr (FP8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           kf[h] = __shfl_sync(0xffffffffu, sc, gid + 8 * h);
-          // the value scale 2^e: e from its exponent bits
-          ev[h] = (float)((int)((__float_as_uint(__shfl_sync(0xffffffffu, sc, 16 + gid + 8 * h)) >> 23) & 255u) - 127);
+          const float sv = __shfl_sync(0xffffffffu, sc, 16 + gid + 8 * h);
+          if constexpr (F32) {
+            // vf 2^ev, 2^ev the next power of two: vf is 1 for a power of two, else in (1/2, 1), or 0 for 0
+            const int e = min(max((int)(((__float_as_uint(sv) & 0x7fffffffu) + 0x7fffffu) >> 23) - 127, -126), 126);
+            ev[h] = (float)e;
+            vf[h] = sv * exp2_int(-e);
+          } else {
+            // its logarithm: whole for a power of two, else off by some 2^-21, far below a half's rounding
+            ev[h] = fast_log2(sv);
+          }
         }
         sc = load_scale(tok_n);
       }
@@ -768,6 +789,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
             const float e = fast_exp2(v - m[nt][x]);
             l[nt][x] += e;
             w[x] = FP8 ? fast_exp2(v + ev[h] - mv[nt][x]) : e;
+            if constexpr (FP8 && F32) w[x] *= vf[h];
           }
           if constexpr (CACHE == kFp32) {
             uint32_t f[3];
@@ -856,7 +878,7 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
     auto chunk_of = [&](int j) { return FP8 ? gid * (D / 32) + j / 2 : CACHE == kBf16 ? 16 * (j >> 2) + 2 * gid + ((j & 3) >> 1) : 8 * (j >> 1) + gid; };
     // a row's outputs over its sum: x times over_sum(); -1 where it saw nothing, and then 0, not 0 * x: x is NaN
     // beside a value of another row that is not finite
-    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? -1.f : (FP8 ? fast_exp2(Mv - M) : 1.f) / L; };
+    auto over_sum = [&](float M, float Mv, float L) { return L == 0.f ? -1.f : (FP8 ? exp2_gradual(Mv - M) : 1.f) / L; };
     auto times = [](float4 x, float f) {
       return f < 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
     };
