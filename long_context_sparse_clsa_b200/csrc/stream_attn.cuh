@@ -36,7 +36,8 @@
 // tiles that adds up (6e-6 of the result over 700 tokens, 4e-7 as it is).  So a tile's products are added to the
 // output, and 16 of d to the score, by fp32 additions.
 // fp32 cache.  Every factor is the exact sum of three bf16 parts; six of the nine products
-// of parts are formed (the others are below 2^-24).  The parts of K and V cost more than the products,
+// of parts are formed.  K's and V's parts are rounded, so that the others, 2^-22.4 of a product at most and 2^-26 as a
+// rule, are of either sign (parts that are all cut off lose 2^-24.7 on the average, always towards zero).  The parts of K and V cost more than the products,
 // so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8: 1345 us; 1550 with 8).
 //
 // The reference (of sums and of outputs) moves only when a score exceeds it by 2^8; then the
@@ -175,10 +176,26 @@ __device__ __forceinline__ void split3(float x, float y, uint32_t& hi, uint32_t&
   mid = __byte_perm(__float_as_uint(mx), __float_as_uint(my), 0x7632u);
   lo = __byte_perm(__float_as_uint(rx - mx), __float_as_uint(ry - my), 0x7632u);
 }
+// as split3, the first two parts rounded to nearest: the parts are smaller (2^-8 and 2^-17 of the number, not 2^-7 and
+// 2^-15) and of either sign.  The largest numbers stay finite, and an infinity goes into the last part.
+__device__ __forceinline__ void split3_near(float x, float y, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  const auto near = [](float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+  };
+  float a, b;
+  hi = near(x, y);
+  unpack_bf16x2(hi, a, b);
+  x -= a, y -= b;
+  mid = near(x, y);
+  unpack_bf16x2(mid, a, b);
+  lo = __byte_perm(__float_as_uint(x - a), __float_as_uint(y - b), 0x7632u);
+}
 __device__ __forceinline__ void add4(float (&a)[4], const float (&b)[4]) {
   a[0] += b[0], a[1] += b[1], a[2] += b[2], a[3] += b[3];
 }
-// the products of parts that reach 2^-24 of the whole, small ones first
+// the products of parts that are formed, small ones first
 __device__ constexpr int kTermA[6] = {2, 0, 1, 1, 0, 0};
 __device__ constexpr int kTermB[6] = {0, 2, 1, 0, 1, 0};
 
@@ -665,8 +682,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
           uint32_t a[3][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            split3(__uint_as_float(w0[2 * e]), __uint_as_float(w0[2 * e + 1]), a[0][2 * e], a[1][2 * e], a[2][2 * e]);
-            split3(__uint_as_float(w1[2 * e]), __uint_as_float(w1[2 * e + 1]), a[0][2 * e + 1], a[1][2 * e + 1], a[2][2 * e + 1]);
+            split3_near(__uint_as_float(w0[2 * e]), __uint_as_float(w0[2 * e + 1]), a[0][2 * e], a[1][2 * e], a[2][2 * e]);
+            split3_near(__uint_as_float(w1[2 * e]), __uint_as_float(w1[2 * e + 1]), a[0][2 * e + 1], a[1][2 * e + 1], a[2][2 * e + 1]);
           }
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -830,8 +847,8 @@ __device__ void kernel_body(const Maps& maps, const Params& p) {
             uint32_t a[3][4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              split3(__uint_as_float(va[2 * w + e]), __uint_as_float(vb2[2 * w + e]), a[0][e], a[1][e], a[2][e]);
-              split3(__uint_as_float(vc[2 * w + e]), __uint_as_float(vd[2 * w + e]), a[0][2 + e], a[1][2 + e], a[2][2 + e]);
+              split3_near(__uint_as_float(va[2 * w + e]), __uint_as_float(vb2[2 * w + e]), a[0][e], a[1][e], a[2][e]);
+              split3_near(__uint_as_float(vc[2 * w + e]), __uint_as_float(vd[2 * w + e]), a[0][2 + e], a[1][2 + e], a[2][2 + e]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
