@@ -1126,16 +1126,8 @@ inline int row_tiles(int R, bool f32) { return R <= 8 || f32 ? 1 : 2; }
 
 // 2-D map of bytes [rows][row_bytes], boxes of 16 rows and up to 128 bytes
 inline bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes, uint32_t box_bytes) {
-  using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static EncodeFn fn = nullptr;
-  if (!fn) {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult st;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &st) != cudaSuccess || !f) return false;
-    fn = reinterpret_cast<EncodeFn>(f);
-  }
+  const TmapEncodeFn fn = tmap_encode_fn();
+  if (!fn) return false;
   const cuuint64_t dims[2] = {row_bytes, rows}, strides[1] = {row_bytes};
   const cuuint32_t box[2] = {box_bytes, kTile}, es[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, es,

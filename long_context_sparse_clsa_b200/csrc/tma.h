@@ -11,6 +11,12 @@
 
 namespace clsa {
 
+// cuTensorMapEncodeTiled, looked up once; null where the driver has none
+using TmapEncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TmapEncodeFn tmap_encode_fn();
+
 // 2-D bf16 tensor [rows][cols] (row-major, row pitch `pitch_bytes`), box = box_cols x
 // box_rows, 128-byte swizzle (box_cols * 2 must be 128).  Out-of-range rows read zero.
 bool make_tmap_bf16_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t pitch_bytes,
