@@ -351,7 +351,7 @@ CLSA_API clsa_status clsa_kv8_read(const clsa_kv8_cache* cache, const int32_t* s
  * its own count or selection).  A row that sees no token gets O = 0 and lse = -inf.
  * Scales are 0 or numbers from 2^-100 to 2^119 (clsa_kv8_write's are powers of two).  Scores, sums and outputs
  * accumulate in fp32; probabilities enter the second product as halves relative to the row's
- * largest (two halves, 22 bits, for fp32).  Deterministic.  One launch.
+ * largest (for fp32 two halves: 22 bits, but no finer than 2^-32 of the largest).  Deterministic.  One launch.
  * CLSA_ERR_UNSUPPORTED: Hq no multiple of Hkv, L Hq > 2^24, B L Hq > 2^27, cache.B n_max > 2^31 - 4096, or
  * over 2e9 tiles of 16 tokens by 8 rows of a KV head.
  * ws: clsa_kv8_attn_workspace_size(a) bytes (0: arguments the call would reject). */
@@ -381,7 +381,8 @@ CLSA_API clsa_status clsa_kv8_attn(const clsa_kv8_attn_args* a, void* ws, size_t
  * part of it, whatever their bytes.  Among those that some row sees, a NaN or infinity in V
  * can reach other rows of the call too (0 * NaN); K's stay with the rows that see them.
  * O [B][T][Hq][d] and lse [B][T][Hq] (fp32, natural log, may be NULL) out; query head h reads
- * KV head h / (Hq / Hkv).  dtype bf16 or fp32 (fp32 products).  Deterministic.  One launch.
+ * KV head h / (Hq / Hkv).  dtype bf16 (probabilities enter the second product as bf16) or fp32 (products and sums
+ * to fp32's precision; an infinity that a row sees can make its result NaN).  Deterministic.  One launch.
  * CLSA_ERR_UNSUPPORTED: Hq no multiple of Hkv or Hq / Hkv > 128, Hkv > 2^16, T Hq > 2^27, B T Hq > 2^30, B n_max > 2^31 - 4096,
  * or over 2e9 tiles of 16 tokens by 8 rows of a KV head.
  * ws: clsa_window_attn_workspace_size(a) bytes (0: arguments the call would reject). */

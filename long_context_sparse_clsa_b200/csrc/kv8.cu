@@ -160,8 +160,8 @@ struct WriteParams {
 // their maximum and their codes, so they are read once.  A thread holds NU units of 16 elements.  No two CTAs share a
 // block's scale or codes.
 // Elements are handled two at a time (packed maximum and product), and those that are not finite only where
-// the maximum shows one: 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64, take 27.5 us; 37.0 one
-// element at a time, with the integer pipe the bound.  2 x 16384 rows: bf16 30.3 us, 6.6 TB/s, fp32 49.4 (56.6
+// the maximum shows one: 4 chunks of 4K to 8K rows of 8 x 128 in bf16, blocks of 64, take 28 us; 37 one
+// element at a time, with the integer pipe the bound.  2 x 16384 rows: bf16 33.1 us, 6.1 TB/s, fp32 50.6 (57
 // with loads of 16 bytes, of which a lane takes every fourth).  Registers are held to eight CTAs an SM:
 // with 54 instead of 32 the first figure was 33.
 template <typename T, int NU, int GS>
@@ -272,7 +272,8 @@ struct ReadParams {
 
 // A thread keeps its place in the row (threadIdx.x: 16 codes of a head, threadIdx.y: the head,
 // blockIdx.y: K or V and the heads behind blockDim.y) and walks the rows of the CTA, kReadRows of
-// them in flight: no divisions in the loop.  4 x 8001 rows of 8 x 128 as bf16: 31.6 us, 6.2 TB/s; 33.1
+// them in flight: no divisions in the loop.  4 x 8001 rows of 8 x 128 as bf16: 32.5 us, 6.0 TB/s, of an index list
+// 34.8 (inputs in turn that L2 does not hold).  The choices below on one set of inputs, 31.6 us: 33.1
 // with stores of 16 bytes, then 38 with four rows, 44 with eight (more registers, fewer threads), 34.1
 // with one step a CTA, 34.9 with four.  One step where the CTAs all fit at once.
 constexpr int kReadRows = 2;
@@ -344,7 +345,7 @@ int log2_of(int x) {
 template <typename T>
 cudaError_t launch_write(WriteParams p, cudaStream_t s) {
   // a block of 16 x 64 has 64 units: a CTA takes four heads (2 x 16384 rows of 8 x 64 in such blocks: 22
-  // us; 67 with a head a CTA, most of its threads idle)
+  // to 24 us; 67 with a head a CTA, most of its threads idle)
   const int units = p.block * (p.d / 16), gs = std::min(8, log2_of(units));
   p.hgroups = (p.Hkv + (kThreadsW >> gs) - 1) >> (8 - gs);
   const dim3 grid((unsigned)(2LL * p.hgroups * p.jmax * p.B));

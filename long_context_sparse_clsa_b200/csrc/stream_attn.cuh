@@ -10,10 +10,12 @@
 // on an SM at d = 128); an index list's by plain loads into the registers that feed the tensor
 // core, one tile ahead (through a ring of asynchronous copies 24 layers over 2048 tokens took
 // 17.4 us, by loads 16.3).
-// Measured (32 heads on 8, d = 128): 131072 tokens of the 8-bit cache 49.5 us, 5.4 TB/s, of which the
-// loop takes 41, at the rate of a plain copy, and 8 go to the launch, the plan and the merge; 16
-// sequences of 16K to 128K tokens 277 us, 6.1 TB/s; 1028 bf16 tokens of 16 sequences 13.2 us; 24 layers
-// over 2048 selected tokens 15.5 us, a chain of latencies (plan 1.5, indices and first rows 3, loop 6, merge 4).
+// Measured (32 heads on 8, d = 128; inputs in turn that L2 does not hold): 131072 tokens of the 8-bit cache 50.7
+// us, 5.3 TB/s, of which the loop takes 42, at about the rate of a plain copy, and 8 go to the launch, the plan and the
+// merge (fp32 queries 65); 16 sequences of 16K to 128K tokens, 1.0 M in all, 320 us, 6.4 TB/s; 1028 bf16 tokens
+// of 16 sequences 17.5 us (fp32 37); 24 layers over 2048 selected tokens 18.3 us, a chain of latencies (plan 1.5,
+// indices and first rows 3 to 6, loop 6, merge 4).  Prompt rows over one cache are not its strength: each streams
+// the cache by itself, through L2 (512 rows over 16384 tokens 2.6 ms, over 131072 21 ms).
 //
 // Fragments.  Both products are computed transposed, so that 16 is the token axis and 8 the row
 // axis (R <= 8 rows waste nothing):
@@ -29,16 +31,21 @@
 // row's largest).  The value blocks' scales 2^e go into the exponent: the output is
 // accumulated from 2^(s_j + e_j - n) with a reference n of its own, so halves never lose a
 // block of small scale.  e is whole for the powers of two that the cache's own write makes; of any other scale
-// it has a fraction (bf16 rows), or what is left of it multiplies the weight (fp32 rows).  With fp32 queries Q and P are split into two halves each (22 bits).
-// bf16 rows.  P is rounded to the type of V's operand, halves (2^-12) or bf16 (2^-9 of a weight, which on random
-// values adds to the result at most what its own rounding does); the row's sum takes it as it was.
+// it has a fraction (bf16 rows), or what is left of it multiplies the weight (fp32 rows).  With fp32 queries Q
+// and P are split into two halves each: 22 bits, but no finer than 2^-38 of the row's largest element of Q and 2^-32 of
+// its largest weight, where the second half is subnormal (a weight 2^-16 of the largest keeps 16 bits).
+// bf16 rows.  P is rounded to the type of V's operand, since a product's factors have one type: to halves (off by up
+// to 2^-11 of a weight) or bf16 (2^-8); the row's sum takes it as it was.  Against 64 bits the result over the 8-bit cache
+// is then off by 1.01 times what weights in fp32 leave, that over bf16 rows by 1.3 to 1.4 times (0.0022 of the
+// result for 0.0016, the output's own rounding).
 // fp32 rows.  The tensor core cuts its sums off instead of rounding them, always towards zero; over many
 // tiles that adds up (6e-6 of the result over 700 tokens, 4e-7 as it is).  So a tile's products are added to the
 // output, and 16 of d to the score, by fp32 additions.
 // fp32 cache.  Every factor is the exact sum of three bf16 parts; six of the nine products
 // of parts are formed.  K's and V's parts are rounded, so that the others, 2^-22.4 of a product at most and 2^-26 as a
-// rule, are of either sign (parts that are all cut off lose 2^-24.7 on the average, always towards zero).  The parts of K and V cost more than the products,
-// so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8: 1345 us; 1550 with 8).
+// rule, are of either sign (parts that are all cut off lose 2^-24.7 on the average, always towards zero).  The
+// parts of K and V cost more than the products, so rows beyond 8 go 16 to a unit (T = 2048, W = 1024, 32 heads on 8:
+// 1390 us; 13 % less than with 8).
 //
 // The reference (of sums and of outputs) moves only when a score exceeds it by 2^8; then the
 // sums are rescaled.  A row's largest p is at least 2^0, at most 2^8: no overflow.  Where p becomes
@@ -49,8 +56,8 @@
 // side.  Few units of like length get whole CTAs each; else all units' tiles form one line that the
 // CTAs share equally, so ragged lengths balance.  A unit that several CTAs share is merged by the one
 // that arrives last, in CTA order (the result does not depend on who that is).  Many units go to a
-// warp each, which shares nothing with the others (fp32, 8 rows a unit, T = 742, W = 6: 11 us, against
-// 33 with CTAs).
+// warp each, which shares nothing with the others (fp32, T = 742, W = 6, 32 heads on 8: 31 us, against
+// 102 with CTAs).
 #pragma once
 
 #include <cuda.h>
@@ -209,7 +216,7 @@ __device__ __forceinline__ int warp_scan_int(int v, int lane) {  // sum over the
 }
 __device__ __forceinline__ int warp_sum_int(int v) { return __reduce_add_sync(0xffffffffu, v); }
 
-// 2^x, subnormal results kept: all the value scales of a row may be 2^-100 and less
+// 2^x, subnormal results kept: the scales of all the values that a row sees may be near 2^-100
 __device__ __forceinline__ float exp2_gradual(float x) {
   const bool low = x < -64.f;
   return fast_exp2(low ? x + 64.f : x) * (low ? 0x1p-64f : 1.f);
@@ -1169,9 +1176,11 @@ cudaError_t launch(Params p, void* ws_body, cudaStream_t s) {
   p.nh = p.Hkv / p.HG;
   p.PG = P / p.HG;
   // More units than CTAs: a unit per warp, unless its rounds fit the warps badly.  Besides its tiles, a
-  // warp's share of HBM each, a unit costs a CTA about 6.5 us and a warp 3.  (8-bit cache, 900 sequences
-  // of 512 tokens, 32 heads on 8: 181 us, 330 with CTAs; 40 of 1000: 65 and 33; 64 of 4096: 246 and 107.
-    // fp32 windows of 8 rows a unit, T = 2048, W = 1024, 32 on 8: 1554 and 2134; 8 on 2, 1.7 rounds: 391 and 525.)
+  // warp's share of HBM each, a unit is taken to cost a CTA 6.5 us and a warp 3 (fitted; a CTA's lie between 3.6, short
+  // units, and 6).  A unit per warp and per CTA, us, 32 heads on 8, d = 128: 8-bit cache, 900 sequences of 512 tokens
+  // 180 and 330; 900 of 64 42 and 183; 200 of 1000 72 and 119; 40 of 1000 68 and 36; 64 of 4096 258 and 108; bf16
+  // windows of 300, T = 4, 200 sequences 68 and 106; fp32 windows, T = 2048, W = 1024 1390 and 1592, W = 64 158 and 334,
+  // 8 heads on 2 (1.7 rounds) 559 and 403.  All chosen right; not so 40 sequences of 200 tokens: 18 and 25, by CTAs.
   const double units = (double)p.B * p.nrg * p.nh, rounds = units / ((double)p.PG * C::W);
   const double tiles_us = most_tiles(p, C::ROWS) * (C::STAGE * C::W / 44e3);
   const bool solo = units > p.PG && std::ceil(rounds) * (3 + tiles_us) < rounds * (6.5 * C::W + tiles_us);

@@ -47,12 +47,12 @@ auto dispatch(const clsa_window_args* a, int R, F&& f) {
 }
 
 // Which form is faster, by a fit to both over T = 2 to 512, windows 64 to 4096, 1 and 3 sequences and six
-// head layouts: of 352 shapes with more than 16 rows it picks one that is over 15 % slower 8 times, and on the
-// average loses 0.7 % (us, 148 SMs).  The streaming form: a start, 1.5e-3 per (16 rows, 16 tokens) at
+// head layouts: of 352 shapes with more than 16 rows it picks one that is over 15 % slower 7 times, and on the
+// average loses 0.8 % (us, 148 SMs).  The streaming form: a start, 1.5e-3 per (16 rows, 16 tokens) at
 // d = 128, more where so many units share the SMs that a CTA goes through several.  The tcgen05
 // form: per round of the SMs 2, and 1.45 (items of one row tile: 1.35) per token tile, however few
-// SMs have an item.  E.g. 32 heads on 8, d = 128: T = 24, W = 4096 25 streaming and 51; T = 96, W = 1024
-// 30 and 18; 6 on 3, d = 64: T = 48, W = 4096 12 and 46; T = 512, W = 1024 28 and 16.
+// SMs have an item.  E.g. 32 heads on 8, d = 128: T = 24, W = 4096 25 streaming and 52; T = 96, W = 1024
+// 30 and 18; 6 on 3, d = 64: T = 48, W = 4096 13 and 45; T = 512, W = 1024 28 and 16.
 bool use_tc(const clsa_window_args* a) {
   if (!window_tc_supported(a) || (long long)a->T * (a->Hq / a->Hkv) <= 16) return false;  // 16 rows: HBM is the bound
   const double G = a->Hq / a->Hkv, TQ = 128 / (a->Hq / a->Hkv), sms = std::max(1, device_info().sm_count);

@@ -24,16 +24,19 @@
 // item too) is issued right behind P V, which the in-order tensor pipe keeps from
 // overwriting P early.  m is a reference that moves only when a score exceeds it by 2^8;
 // then O is rescaled in TMEM.  A row's softmax needs no exchange: its 128 scores are one lane.
-// P is rounded to bf16, since an MMA's operands have one type and V's is bf16: up to 2^-9 of each weight,
-// which on random values adds to the result at most what its own rounding to bf16 does.  The row's sum
-// takes the weights as they were.
+// P is rounded to bf16, since an MMA's operands have one type and V's is bf16: off by up to 2^-8 of each weight.
+// On random values the result's error against 64 bits is then 1.3 to 1.4 times that of weights in fp32 (0.0022 of the
+// result for 0.0016, its own rounding to bf16).  The row's sum takes the weights as they were.
 // Bound: per token tile and row tile 2 x 128 x 128 x d multiplies and 128 x 128 exponentials, which at
 // d = 128 take the tensor cores and the special-function units about 1024 cycles each.
-// Measured (32 heads on 8, d = 128): T = 16381, W = 4096 840 us, 1.15 PFLOP/s of visible products; T = 4096,
-// W = 1024 75 us, 0.92 PFLOP/s.  A step of both row tiles takes about 2950 cycles: 1450 for a tile's
+// Measured (32 heads on 8, d = 128; inputs in turn that L2 does not hold): T = 16381, W = 4096 750 us, 1.28 PFLOP/s
+// of visible products, over some ms, 860 over longer runs at the power limit; T = 4096, W = 1024 78.5 us, 0.88 PFLOP/s
+// (75 with its inputs in L2).  A step of both row tiles takes about 2950 cycles: 1450 for a tile's
 // exponentials and P, 400 for its scores and maximum, then 920 until P V and the next S are through
 // (768 of them products); the two tiles' chains overlap, but neither pipe fills (tensor cores active 49 %
-// at W = 1024).  A change of item costs about 5000 cycles more, partly filled tiles the rest.
+// at W = 1024).  P leaves columns 64 to 127 of each S free, so half of a tile's next scores could be in TMEM before P V
+// has read this one's; they are all issued behind it.  A change of item costs about 5000 cycles more, partly filled
+// tiles the rest.
 //
 // Every wait is bounded; one that runs out records CLSA_ERR_TIMEOUT and the CTA drains its
 // loads and returns.
