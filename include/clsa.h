@@ -320,7 +320,7 @@ typedef struct clsa_kv8_cache {
 
 /* Quantise new rows K, V [B][T][Hkv][d] (dt) into the cache: row t < count[b] of sequence b
  * becomes token start[b] + t (count NULL: T rows; counts are clamped to [0, T]).  Codes are
- * x / scale rounded to nearest even; infinities saturate to +-448, NaN is kept.  Tokens before
+ * x / scale (in fp32, exact for powers of two) rounded to nearest even; infinities saturate to +-448, NaN is kept.  Tokens before
  * start[b] count as written, tokens from start[b] on as free: a block whose first token is
  * among the new rows gets a new scale; a block that holds earlier rows keeps its scale or
  * takes a larger one, and then its earlier codes are rounded to that.  Tokens behind the new
